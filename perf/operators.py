@@ -269,7 +269,8 @@ def _quant(x, dim):
     s = ((mx - mn) / 15).bfloat16().float()
     s = torch.where(s < 2.0 ** -100, torch.zeros_like(s), s)
     z = (mn.double() - 16 * s.double()).float().bfloat16().float()
-    c = torch.round((x - z) / torch.where(s == 0, torch.ones_like(s), s)) - 16
+    # which code is nearest is decided in 64 bits
+    c = torch.round((x.double() - z) / torch.where(s == 0, torch.ones_like(s), s)) - 16
     c = torch.where(s == 0, torch.zeros_like(c), c).clamp(0, 15)
     return s, z, c.to(torch.int32)
 
