@@ -6,7 +6,7 @@ script (``build.py``).
 """
 from .binding import (  # noqa: F401
     HGA_BF16, HGA_FP32, HGA_DEV_BAD_INDEX, HGA_DEV_TIMEOUT, HGA_DEV_STAGE_FULL, HGA_TIER_RESET, HGA_TIER_CHAIN,
-    EXPORTED, HGAError, Params, TierSched, lib,
+    EXPORTED, HGAError, Params, ProjParams, TierSched, lib,
     hga_build_summaries, hga_route, hga_route_causal, hga_route_groups, hga_route_groups_tiered, hga_attn_fwd,
     hga_route_attn_fwd,
     hga_attn_bwd_workspace_size,
@@ -15,5 +15,6 @@ from .binding import (  # noqa: F401
     hga_attn_bwd_causal,
     hga_tier_scratch_size, hga_tier_reset, hga_fetch_tiered, hga_tier_offload, hga_attn_fwd_tiered,
     hga_segment_fwd_tiered, hga_segment_fwd,
+    hga_rope_table, hga_qk_norm_rope, hga_qk_norm_rope_workspace_size, hga_qk_norm_rope_bwd,
     hga_get_device_status, hga_selftest_wait_timeout,
 )

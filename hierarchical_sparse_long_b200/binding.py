@@ -29,7 +29,8 @@ EXPORTED = ("hga_build_summaries", "hga_route", "hga_route_causal", "hga_route_g
             "hga_attn_causal_workspace_size", "hga_attn_fwd_causal", "hga_attn_bwd_causal",
             "hga_attn_bwd_noalloc", "hga_attn_decode_workspace_size", "hga_attn_decode", "hga_tier_scratch_size",
             "hga_tier_reset", "hga_fetch_tiered", "hga_tier_offload", "hga_attn_fwd_tiered", "hga_segment_fwd_tiered",
-            "hga_segment_fwd",
+            "hga_segment_fwd", "hga_rope_table", "hga_qk_norm_rope", "hga_qk_norm_rope_workspace_size",
+            "hga_qk_norm_rope_bwd",
             "hga_get_device_status", "hga_selftest_wait_timeout", "hga_status_string", "hga_last_error")
 
 
@@ -73,6 +74,40 @@ class Params:
         return CParams(self.batch, self.n_q_heads, self.n_kv_heads, self.head_dim, self.chunk, self.q_block,
                        self.topk, self.seg_len, self.n_hist_chunks, self.dtype, hs, ss, self.qblock_begin,
                        self.qblock_end, self.sink_chunks)
+
+
+class CProj(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("n_q_heads", ctypes.c_int), ("n_kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("seq_len", ctypes.c_int), ("rotary_dim", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("eps", ctypes.c_float), ("q_token_stride", ctypes.c_longlong),
+                ("k_token_stride", ctypes.c_longlong), ("v_token_stride", ctypes.c_longlong),
+                ("kv_head_stride", ctypes.c_longlong), ("first_pos", ctypes.c_longlong)]
+
+
+@dataclasses.dataclass
+class ProjParams:
+    """Mirror of ``hga_proj_t`` (token strides in elements, -1: rows of one fused
+    projection of (Hq + 2 Hkv) * D; kv_head_stride in tokens, -1: seq_len)."""
+    batch: int
+    n_q_heads: int
+    n_kv_heads: int
+    head_dim: int
+    seq_len: int
+    rotary_dim: int
+    dtype: int = HGA_BF16
+    eps: float = 1e-6
+    q_token_stride: int = -1
+    k_token_stride: int = -1
+    v_token_stride: int = -1
+    kv_head_stride: int = -1
+    first_pos: int = 0
+
+    def c(self) -> CProj:
+        row = (self.n_q_heads + 2 * self.n_kv_heads) * self.head_dim
+        st = [s if s >= 0 else row for s in (self.q_token_stride, self.k_token_stride, self.v_token_stride)]
+        ks = self.kv_head_stride if self.kv_head_stride >= 0 else self.seq_len
+        return CProj(self.batch, self.n_q_heads, self.n_kv_heads, self.head_dim, self.seq_len, self.rotary_dim,
+                     self.dtype, self.eps, *st, ks, self.first_pos)
 
 
 _lib = None
@@ -119,6 +154,12 @@ def lib() -> ctypes.CDLL:
                                       ctypes.POINTER(_TierSchedC)]
         L.hga_segment_fwd_tiered.argtypes = [pp, vp, vp, vp, vp, vp, vp, i, vp, vp, vp, vp, vp, vp, vp, i, vp, vp, i,
                                              i, vp, vp, vp, vp, vp, ctypes.POINTER(_TierSchedC)]
+        pj = ctypes.POINTER(CProj)
+        L.hga_rope_table.argtypes = [ctypes.c_double, i, ll, vp, vp]
+        L.hga_qk_norm_rope.argtypes = [pj, vp, vp, vp, vp, vp, vp, ll, vp, vp, vp, vp, vp]
+        L.hga_qk_norm_rope_workspace_size.argtypes = [pj]
+        L.hga_qk_norm_rope_workspace_size.restype = sz
+        L.hga_qk_norm_rope_bwd.argtypes = [pj, vp, vp, vp, vp, vp, ll, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
         L.hga_get_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint)]
         L.hga_selftest_wait_timeout.argtypes = [ll, vp]
         L.hga_selftest_wait_timeout.restype = ctypes.c_int
@@ -130,6 +171,7 @@ def lib() -> ctypes.CDLL:
                   "hga_attn_bwd", "hga_attn_bwd_noalloc", "hga_attn_fwd_groups", "hga_attn_bwd_groups",
                   "hga_route_attn_fwd",
                   "hga_attn_fwd_causal", "hga_attn_bwd_causal",
+                  "hga_rope_table", "hga_qk_norm_rope", "hga_qk_norm_rope_bwd",
                   "hga_attn_decode", "hga_tier_reset", "hga_fetch_tiered", "hga_tier_offload", "hga_attn_fwd_tiered",
                   "hga_get_device_status"):
             getattr(L, f).restype = ctypes.c_int
@@ -437,6 +479,42 @@ def hga_selftest_wait_timeout(wait_cycles: int, stream=None):
     """Launches a wait that can never complete, bounded to wait_cycles; the device
     status then carries HGA_DEV_TIMEOUT (see hga_get_device_status)."""
     _check(lib().hga_selftest_wait_timeout(wait_cycles, _stream(stream)), "hga_selftest_wait_timeout")
+
+
+def hga_rope_table(theta: float, rotary_dim: int, n_pos: int, table, stream=None):
+    """cos / sin rows of positions [0, n_pos) into table [n_pos][rotary_dim] (fp32)."""
+    _check(lib().hga_rope_table(theta, rotary_dim, n_pos, _ptr(table), _stream(stream)), "hga_rope_table")
+
+
+def _table_rows(p: ProjParams, table) -> int:
+    return 0 if table is None or p.rotary_dim == 0 else table.numel() // p.rotary_dim
+
+
+def hga_qk_norm_rope(p: ProjParams, q, k, v, q_weight, k_weight, table, positions, q_out, k_out, v_out, stream=None):
+    """Per-head norm of q and k, position rotation and head-major layout of q, k and v from a
+    layer's projections; positions int32 [B][S] (-1: padding row) or None for p.first_pos + i."""
+    cp = p.c()
+    _check(lib().hga_qk_norm_rope(ctypes.byref(cp), _ptr(q), _ptr(k), _ptr(v), _ptr(q_weight), _ptr(k_weight),
+                                  _ptr(table), _table_rows(p, table), _ptr(positions), _ptr(q_out), _ptr(k_out),
+                                  _ptr(v_out), _stream(stream)), "hga_qk_norm_rope")
+
+
+def hga_qk_norm_rope_workspace_size(p: ProjParams) -> int:
+    cp = p.c()
+    return int(lib().hga_qk_norm_rope_workspace_size(ctypes.byref(cp)))
+
+
+def hga_qk_norm_rope_bwd(p: ProjParams, q, k, q_weight, k_weight, table, positions, dq, dk, dv, dq_in, dk_in, dv_in,
+                         dq_weight, dk_weight, workspace, stream=None):
+    """Backward of hga_qk_norm_rope: gradients of the projections (dtype) and of the weights (fp32)
+    from the attention's fp32 dq, dk, dv."""
+    cp = p.c()
+    nbytes = workspace.numel() * workspace.element_size()
+    _check(lib().hga_qk_norm_rope_bwd(ctypes.byref(cp), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight),
+                                      _ptr(table), _table_rows(p, table), _ptr(positions), _ptr(dq), _ptr(dk),
+                                      _ptr(dv), _ptr(dq_in), _ptr(dk_in), _ptr(dv_in), _ptr(dq_weight),
+                                      _ptr(dk_weight), _ptr(workspace), nbytes, _stream(stream)),
+           "hga_qk_norm_rope_bwd")
 
 
 def hga_get_device_status(stream=None) -> int:

@@ -737,6 +737,90 @@ hga_status_t hga_segment_fwd(const hga_params_t *p, const void *q, const void *k
     return HGA_OK;
 }
 
+namespace {
+
+hga_status_t check_proj(const hga_proj_t *p) {
+    if (!p) return HGA_ERR_INVALID_ARG;
+    if (p->batch < 1 || p->n_q_heads < 1 || p->n_kv_heads < 1 || p->seq_len < 1) return HGA_ERR_INVALID_ARG;
+    if (p->dtype != HGA_BF16 && p->dtype != HGA_FP32) return HGA_ERR_INVALID_ARG;
+    if (p->head_dim != 64 && p->head_dim != 128) return HGA_ERR_UNSUPPORTED;
+    if (p->rotary_dim < 0 || p->rotary_dim > p->head_dim || p->rotary_dim % 16) return HGA_ERR_INVALID_ARG;
+    if (!(p->eps > 0.f) || !std::isfinite(p->eps)) return HGA_ERR_INVALID_ARG;
+    const int vec = p->dtype == HGA_FP32 ? 4 : 8;
+    const long long strides[3] = {p->q_token_stride, p->k_token_stride, p->v_token_stride};
+    for (int i = 0; i < 3; ++i) {
+        const long long heads = i == 0 ? p->n_q_heads : p->n_kv_heads;
+        if (strides[i] < heads * p->head_dim || strides[i] % vec) return HGA_ERR_INVALID_ARG;
+    }
+    // grid limits: token groups along x, head groups along y
+    if ((long long)p->batch * p->seq_len >= (1ll << 31) || p->n_q_heads > 16384 || p->n_kv_heads > 16384)
+        return HGA_ERR_UNSUPPORTED;
+    return HGA_OK;
+}
+
+// table / positions of a call: a null positions needs first_pos .. first_pos + S in the table
+hga_status_t check_rotation(const hga_proj_t *p, const float *table, long long n_pos, const int32_t *positions) {
+    if (p->rotary_dim > 0 && (!table || !aligned16(table) || n_pos < 1)) return HGA_ERR_INVALID_ARG;
+    if (!positions && (p->first_pos < 0 || (p->rotary_dim > 0 && (p->first_pos > n_pos - p->seq_len))))
+        return HGA_ERR_INVALID_ARG;
+    return HGA_OK;
+}
+
+}  // namespace
+
+hga_status_t hga_rope_table(double theta, int rotary_dim, long long n_pos, float *table, cudaStream_t stream) {
+    CallRange range("hga_rope_table");
+    if (!(theta > 0.0) || !std::isfinite(theta) || rotary_dim < 16 || rotary_dim > 128 || rotary_dim % 16 ||
+        n_pos < 0 || n_pos >= (1ll << 32))
+        return HGA_ERR_INVALID_ARG;
+    if (n_pos == 0) return HGA_OK;
+    if (!table || !aligned16(table)) return HGA_ERR_INVALID_ARG;
+    return hga::launch_rope_table(theta, rotary_dim, n_pos, table, stream);
+}
+
+hga_status_t hga_qk_norm_rope(const hga_proj_t *p, const void *q, const void *k, const void *v, const void *q_weight,
+                              const void *k_weight, const float *table, long long n_pos, const int32_t *positions,
+                              void *q_out, void *k_out, void *v_out, cudaStream_t stream) {
+    CallRange range("hga_qk_norm_rope");
+    hga_status_t st = check_proj(p);
+    if (st != HGA_OK) return st;
+    if (p->kv_head_stride < p->seq_len) return HGA_ERR_INVALID_ARG;
+    st = check_rotation(p, table, n_pos, positions);
+    if (st != HGA_OK) return st;
+    for (const void *ptr : {q, k, v, q_weight, k_weight, (const void *)q_out, (const void *)k_out, (const void *)v_out})
+        if (!ptr || !aligned16(ptr)) return HGA_ERR_INVALID_ARG;
+    unsigned *status = status_ptr();
+    if (!status) return hga::record_cuda(cudaErrorInvalidDevice);
+    return hga::launch_qk_norm_rope(*p, q, k, v, q_weight, k_weight, table, n_pos, positions, q_out, k_out, v_out,
+                                    status, stream);
+}
+
+size_t hga_qk_norm_rope_workspace_size(const hga_proj_t *p) {
+    if (check_proj(p) != HGA_OK) return 0;
+    return hga::qk_norm_rope_workspace_bytes(*p);
+}
+
+hga_status_t hga_qk_norm_rope_bwd(const hga_proj_t *p, const void *q, const void *k, const void *q_weight,
+                                  const void *k_weight, const float *table, long long n_pos,
+                                  const int32_t *positions, const float *dq, const float *dk, const float *dv,
+                                  void *dq_in, void *dk_in, void *dv_in, float *dq_weight, float *dk_weight,
+                                  void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    CallRange range("hga_qk_norm_rope_bwd");
+    hga_status_t st = check_proj(p);
+    if (st != HGA_OK) return st;
+    st = check_rotation(p, table, n_pos, positions);
+    if (st != HGA_OK) return st;
+    for (const void *ptr : {q, k, q_weight, k_weight, (const void *)dq, (const void *)dk, (const void *)dv,
+                            (const void *)dq_in, (const void *)dk_in, (const void *)dv_in, (const void *)workspace})
+        if (!ptr || !aligned16(ptr)) return HGA_ERR_INVALID_ARG;
+    if (!dq_weight || !dk_weight || workspace_bytes < hga::qk_norm_rope_workspace_bytes(*p)) return HGA_ERR_INVALID_ARG;
+    unsigned *status = status_ptr();
+    if (!status) return hga::record_cuda(cudaErrorInvalidDevice);
+    return hga::launch_qk_norm_rope_bwd(*p, q, k, q_weight, k_weight, table, n_pos, positions, dq, dk, dv, dq_in,
+                                        dk_in, dv_in, dq_weight, dk_weight, static_cast<float *>(workspace), status,
+                                        stream);
+}
+
 hga_status_t hga_selftest_wait_timeout(long long wait_cycles, cudaStream_t stream) {
     CallRange range("hga_selftest_wait_timeout");
     if (wait_cycles < 1000 || wait_cycles > (1ll << 32)) return HGA_ERR_INVALID_ARG;

@@ -150,6 +150,17 @@ hga_status_t launch_fetch_tiered(const hga_params_t &p, const void *host_k, cons
                                  int stage_slots, int lag, int32_t *scratch, int32_t *idx_remapped,
                                  int32_t *n_fetched, unsigned *status, cudaStream_t stream,
                                  const void *prev_k = nullptr, const void *prev_v = nullptr);
+// Projections to attention inputs (qk_norm_rope.cu).
+hga_status_t launch_rope_table(double theta, int rotary_dim, long long n_pos, float *table, cudaStream_t stream);
+hga_status_t launch_qk_norm_rope(const hga_proj_t &p, const void *q, const void *k, const void *v, const void *qw,
+                                 const void *kw, const float *table, long long n_pos, const int32_t *positions,
+                                 void *q_out, void *k_out, void *v_out, unsigned *status, cudaStream_t stream);
+size_t qk_norm_rope_workspace_bytes(const hga_proj_t &p);
+hga_status_t launch_qk_norm_rope_bwd(const hga_proj_t &p, const void *q, const void *k, const void *qw,
+                                     const void *kw, const float *table, long long n_pos, const int32_t *positions,
+                                     const float *dq, const float *dk, const float *dv, void *dq_in, void *dk_in,
+                                     void *dv_in, float *dqw, float *dkw, float *ws, unsigned *status,
+                                     cudaStream_t stream);
 hga_status_t launch_selftest_wait_timeout(long long wait_cycles, unsigned *status, cudaStream_t stream);
 hga_status_t record_cuda(cudaError_t e);
 void record_error(const char *msg);

@@ -538,6 +538,83 @@ hga_status_t hga_segment_fwd(const hga_params_t *p, const void *q, const void *k
                              void *out, float *lse, int flags, cudaStream_t stream, cudaStream_t route_stream,
                              hga_tier_sched_t *sched);
 
+/* Shape of the projections of one layer call (hga_qk_norm_rope).
+ *   batch B, n_q_heads Hq, n_kv_heads Hkv, head_dim D (64 or 128), seq_len S
+ *   (1 .. ; any length), dtype of the projections, the weights and q / k / v.
+ *   rotary_dim R: the first R dims of every head are rotated (0 .. D, a
+ *     multiple of 16; 0: norms only), as pairs (i, i + R/2).
+ *   eps: added to the mean square (> 0).
+ *   q_token_stride / k_token_stride / v_token_stride: elements between the rows
+ *     of consecutive tokens of q / k / v (token (b, i) is row b*S + i), at least
+ *     heads * D and a multiple of 16 bytes.  One fused projection is three
+ *     pointers into the same rows.
+ *   kv_head_stride: tokens between (b, g) slices of k_out / v_out (>= S).
+ *   first_pos: position of token 0 of every sequence when positions is null. */
+typedef struct {
+    int batch;
+    int n_q_heads;
+    int n_kv_heads;
+    int head_dim;
+    int seq_len;
+    int rotary_dim;
+    hga_dtype_t dtype;
+    float eps;
+    long long q_token_stride;
+    long long k_token_stride;
+    long long v_token_stride;
+    long long kv_head_stride;
+    long long first_pos;
+} hga_proj_t;
+
+/* Rotation table: table[pos*R + i] = cos(a), table[pos*R + R/2 + i] = sin(a) with
+ * a = pos * theta^(-2 i / R), i < R/2, pos < n_pos; angles in 64 bits, rounded once
+ * to fp32.  A plan made once per model; other frequency rules fill the same layout.
+ *   rotary_dim: a multiple of 16, 16 .. 128.  theta > 0.  n_pos * R/2 < 2^38.
+ *   table: device fp32 [n_pos][R], 16-byte aligned.  n_pos == 0 is a no-op. */
+hga_status_t hga_rope_table(double theta, int rotary_dim, long long n_pos, float *table, cudaStream_t stream);
+
+/* From a layer's projections to the attention's inputs (technical summary
+ * section 2.1 takes queries, keys and values per head and position as given):
+ * the RMS norm of every q and k head with a weight per dim, the position
+ * rotation, and the turn from token-major rows to the head-major layout of the
+ * other calls, in one pass.  For head row x of q or k, weight w and position pos:
+ *   n = x * w / sqrt(mean(x^2) + eps)
+ *   y_i = n_i c_i - n_{i+R/2} s_i,  y_{i+R/2} = n_{i+R/2} c_i + n_i s_i   (i < R/2)
+ * with c_i, s_i from row pos of table; dims >= R are n; v is copied.  fp32
+ * arithmetic, one rounding to dtype.
+ *   q, k, v: device, token rows as in hga_proj_t.  q_weight, k_weight: device [D]
+ *     dtype.  table: device fp32 [n_pos][R] (hga_rope_table; may be null for R = 0).
+ *   positions: device int32 [B][S], or null for first_pos + i (then first_pos >= 0
+ *     and, with R > 0, first_pos + S <= n_pos).  -1 marks a padding row: none of
+ *     its outputs is written.  Any other position outside the table is treated
+ *     the same and flagged HGA_DEV_BAD_INDEX.
+ *   q_out: device [B][Hq][S][D].  k_out, v_out: device [B][Hkv][*][D], slices
+ *     kv_head_stride tokens apart: rows [0, S) of each are written, so a pointer
+ *     into a segment or local-window buffer appends the tokens to it.  Outputs
+ *     must not overlap inputs.
+ * S = 1 is the step of a new token of every sequence.  One kernel. */
+hga_status_t hga_qk_norm_rope(const hga_proj_t *p, const void *q, const void *k, const void *v, const void *q_weight,
+                              const void *k_weight, const float *table, long long n_pos, const int32_t *positions,
+                              void *q_out, void *k_out, void *v_out, cudaStream_t stream);
+
+/* Backward of hga_qk_norm_rope.  dq [B][Hq][S][D], dk and dv [B][Hkv][S][D]: device
+ * fp32, as hga_attn_bwd writes them.  With dn the transposed rotation of the
+ * incoming row, r = 1 / sqrt(mean(x^2) + eps), xh = x r and g = dn w:
+ *   dx = r (g - xh mean(g xh)),   dw = sum over every head row of dn xh.
+ *   dq_in, dk_in, dv_in: device dtype, rows and strides of q, k, v (the operands of
+ *     the projections' products, so they are rounded to dtype); padding rows get
+ *     zeros.  dq_weight, dk_weight: device fp32 [D], overwritten.
+ *   q, k, weights, table, positions: the forward's.  kv_head_stride is not used.
+ *   workspace: device, >= hga_qk_norm_rope_workspace_size(p) bytes, 16-byte aligned
+ *     (partial sums of dw; nothing in it needs clearing).
+ * Two kernels; no atomics, so equal inputs give equal bits. */
+size_t hga_qk_norm_rope_workspace_size(const hga_proj_t *p);
+hga_status_t hga_qk_norm_rope_bwd(const hga_proj_t *p, const void *q, const void *k, const void *q_weight,
+                                  const void *k_weight, const float *table, long long n_pos,
+                                  const int32_t *positions, const float *dq, const float *dk, const float *dv,
+                                  void *dq_in, void *dk_in, void *dv_in, float *dq_weight, float *dk_weight,
+                                  void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
 /* Self-test of the bounded waits (the source pages have no counterpart): every
  * pipeline wait in the tensor-core kernels gives up after a cycle limit instead
  * of hanging, sets HGA_DEV_TIMEOUT and lets the kernel end.  This launches one
