@@ -15,6 +15,7 @@ from .binding import (  # noqa: F401
     hga_attn_bwd_causal,
     hga_tier_scratch_size, hga_tier_reset, hga_fetch_tiered, hga_tier_offload, hga_attn_fwd_tiered,
     hga_segment_fwd_tiered, hga_segment_fwd,
+    hga_packed_chunk_bytes, hga_pack_history, hga_unpack_history, hga_attn_fwd_packed, hga_attn_decode_packed,
     hga_rope_table, hga_qk_norm_rope, hga_qk_norm_rope_workspace_size, hga_qk_norm_rope_bwd,
     hga_get_device_status, hga_selftest_wait_timeout,
 )

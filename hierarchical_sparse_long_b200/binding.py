@@ -30,7 +30,8 @@ EXPORTED = ("hga_build_summaries", "hga_route", "hga_route_causal", "hga_route_g
             "hga_attn_bwd_noalloc", "hga_attn_decode_workspace_size", "hga_attn_decode", "hga_tier_scratch_size",
             "hga_tier_reset", "hga_fetch_tiered", "hga_tier_offload", "hga_attn_fwd_tiered", "hga_segment_fwd_tiered",
             "hga_segment_fwd", "hga_rope_table", "hga_qk_norm_rope", "hga_qk_norm_rope_workspace_size",
-            "hga_qk_norm_rope_bwd",
+            "hga_qk_norm_rope_bwd", "hga_packed_chunk_bytes", "hga_pack_history", "hga_unpack_history",
+            "hga_attn_fwd_packed", "hga_attn_decode_packed",
             "hga_get_device_status", "hga_selftest_wait_timeout", "hga_status_string", "hga_last_error")
 
 
@@ -160,6 +161,12 @@ def lib() -> ctypes.CDLL:
         L.hga_qk_norm_rope_workspace_size.argtypes = [pj]
         L.hga_qk_norm_rope_workspace_size.restype = sz
         L.hga_qk_norm_rope_bwd.argtypes = [pj, vp, vp, vp, vp, vp, ll, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.hga_packed_chunk_bytes.argtypes = [i]
+        L.hga_packed_chunk_bytes.restype = sz
+        L.hga_pack_history.argtypes = [vp, vp, ll, i, i, i, i, i, i, vp, i, vp, i, vp]
+        L.hga_unpack_history.argtypes = [vp, i, i, i, i, i, i, i, vp, vp, ll, vp]
+        L.hga_attn_fwd_packed.argtypes = [pp, vp, vp, i, vp, vp, vp, vp, vp, vp]
+        L.hga_attn_decode_packed.argtypes = [pp, vp, vp, i, vp, vp, i, vp, vp, vp, vp]
         L.hga_get_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint)]
         L.hga_selftest_wait_timeout.argtypes = [ll, vp]
         L.hga_selftest_wait_timeout.restype = ctypes.c_int
@@ -172,6 +179,7 @@ def lib() -> ctypes.CDLL:
                   "hga_route_attn_fwd",
                   "hga_attn_fwd_causal", "hga_attn_bwd_causal",
                   "hga_rope_table", "hga_qk_norm_rope", "hga_qk_norm_rope_bwd",
+                  "hga_pack_history", "hga_unpack_history", "hga_attn_fwd_packed", "hga_attn_decode_packed",
                   "hga_attn_decode", "hga_tier_reset", "hga_fetch_tiered", "hga_tier_offload", "hga_attn_fwd_tiered",
                   "hga_get_device_status"):
             getattr(L, f).restype = ctypes.c_int
@@ -515,6 +523,45 @@ def hga_qk_norm_rope_bwd(p: ProjParams, q, k, q_weight, k_weight, table, positio
                                       _ptr(dv), _ptr(dq_in), _ptr(dk_in), _ptr(dv_in), _ptr(dq_weight),
                                       _ptr(dk_weight), _ptr(workspace), nbytes, _stream(stream)),
            "hga_qk_norm_rope_bwd")
+
+
+def hga_packed_chunk_bytes(head_dim: int) -> int:
+    """Bytes of the 4-bit record of one 64-token chunk of one KV head (K and V)."""
+    return int(lib().hga_packed_chunk_bytes(head_dim))
+
+
+def hga_pack_history(k, v, head_stride: int, batch: int, n_kv_heads: int, head_dim: int, first_chunk: int,
+                     n_chunks: int, hist, hist_cap_chunks: int, summ=None, summ_cap_chunks: int = 0, stream=None):
+    """Packs closed chunks (rows 0 .. of k / v) into the 4-bit records [first_chunk, first_chunk +
+    n_chunks) of hist, and appends their summaries when summ is given."""
+    _check(lib().hga_pack_history(_ptr(k), _ptr(v), head_stride, batch, n_kv_heads, head_dim, first_chunk, n_chunks,
+                                  dtype_code(k), _ptr(hist), hist_cap_chunks, _ptr(summ), summ_cap_chunks,
+                                  _stream(stream)), "hga_pack_history")
+
+
+def hga_unpack_history(hist, hist_cap_chunks: int, batch: int, n_kv_heads: int, head_dim: int, first_chunk: int,
+                       n_chunks: int, k, v, head_stride: int, stream=None):
+    """The values of packed chunks [first_chunk, first_chunk + n_chunks) into rows 0 .. of k / v."""
+    _check(lib().hga_unpack_history(_ptr(hist), hist_cap_chunks, batch, n_kv_heads, head_dim, first_chunk, n_chunks,
+                                    dtype_code(k), _ptr(k), _ptr(v), head_stride, _stream(stream)),
+           "hga_unpack_history")
+
+
+def hga_attn_fwd_packed(p: Params, q, hist, hist_cap_chunks: int, k_seg, v_seg, idx, out, lse, stream=None):
+    """hga_attn_fwd over a packed (4-bit) history."""
+    cp = p.c()
+    _check(lib().hga_attn_fwd_packed(ctypes.byref(cp), _ptr(q), _ptr(hist), hist_cap_chunks, _ptr(k_seg),
+                                     _ptr(v_seg), _ptr(idx), _ptr(out), _ptr(lse), _stream(stream)),
+           "hga_attn_fwd_packed")
+
+
+def hga_attn_decode_packed(p: Params, q, hist, hist_cap_chunks: int, k_local, v_local, n_local: int, idx, out, lse,
+                           stream=None):
+    """hga_attn_decode over a packed (4-bit) history; the local window is bf16."""
+    cp = p.c()
+    _check(lib().hga_attn_decode_packed(ctypes.byref(cp), _ptr(q), _ptr(hist), hist_cap_chunks, _ptr(k_local),
+                                        _ptr(v_local), n_local, _ptr(idx), _ptr(out), _ptr(lse), _stream(stream)),
+           "hga_attn_decode_packed")
 
 
 def hga_get_device_status(stream=None) -> int:

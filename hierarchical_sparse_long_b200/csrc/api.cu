@@ -821,6 +821,109 @@ hga_status_t hga_qk_norm_rope_bwd(const hga_proj_t *p, const void *q, const void
                                         stream);
 }
 
+size_t hga_packed_chunk_bytes(int head_dim) {
+    return head_dim == 64 || head_dim == 128 ? (size_t)72 * head_dim : 0;
+}
+
+namespace {
+
+// Shape of a pack / unpack call: chunks [first, first + n) of slices of `stride` tokens.
+hga_status_t check_chunks(int batch, int n_kv_heads, int head_dim, int first_chunk, int n_chunks, hga_dtype_t dtype,
+                          int cap, long long head_stride) {
+    if (batch < 1 || n_kv_heads < 1 || first_chunk < 0 || n_chunks < 0) return HGA_ERR_INVALID_ARG;
+    if (dtype != HGA_BF16 && dtype != HGA_FP32) return HGA_ERR_INVALID_ARG;
+    if (head_dim != 64 && head_dim != 128) return HGA_ERR_UNSUPPORTED;
+    if ((long long)first_chunk + n_chunks > cap || head_stride < (long long)n_chunks * 64) return HGA_ERR_INVALID_ARG;
+    // one CTA per record
+    if ((long long)batch * n_kv_heads >= (1ll << 31) || (long long)batch * n_kv_heads * n_chunks >= (1ll << 31))
+        return HGA_ERR_UNSUPPORTED;
+    return HGA_OK;
+}
+
+}  // namespace
+
+hga_status_t hga_pack_history(const void *k, const void *v, long long head_stride, int batch, int n_kv_heads,
+                              int head_dim, int first_chunk, int n_chunks, hga_dtype_t dtype, void *hist,
+                              int hist_cap_chunks, float *summ, int summ_cap_chunks, cudaStream_t stream) {
+    CallRange range("hga_pack_history");
+    hga_status_t st = check_chunks(batch, n_kv_heads, head_dim, first_chunk, n_chunks, dtype, hist_cap_chunks,
+                                   head_stride);
+    if (st != HGA_OK) return st;
+    if (summ && ((long long)first_chunk + n_chunks > summ_cap_chunks || !aligned16(summ))) return HGA_ERR_INVALID_ARG;
+    if (n_chunks == 0) return HGA_OK;
+    for (const void *ptr : {k, v, (const void *)hist})
+        if (!ptr || !aligned16(ptr)) return HGA_ERR_INVALID_ARG;
+    return hga::launch_pack_history(k, v, head_stride, (long long)batch * n_kv_heads, head_dim, first_chunk, n_chunks,
+                                    dtype, static_cast<uint8_t *>(hist), hist_cap_chunks, summ, summ_cap_chunks,
+                                    stream);
+}
+
+hga_status_t hga_unpack_history(const void *hist, int hist_cap_chunks, int batch, int n_kv_heads, int head_dim,
+                                int first_chunk, int n_chunks, hga_dtype_t dtype, void *k, void *v,
+                                long long head_stride, cudaStream_t stream) {
+    CallRange range("hga_unpack_history");
+    hga_status_t st = check_chunks(batch, n_kv_heads, head_dim, first_chunk, n_chunks, dtype, hist_cap_chunks,
+                                   head_stride);
+    if (st != HGA_OK) return st;
+    if (n_chunks == 0) return HGA_OK;
+    for (const void *ptr : {hist, (const void *)k, (const void *)v})
+        if (!ptr || !aligned16(ptr)) return HGA_ERR_INVALID_ARG;
+    return hga::launch_unpack_history(static_cast<const uint8_t *>(hist), hist_cap_chunks,
+                                      (long long)batch * n_kv_heads, head_dim, first_chunk, n_chunks, dtype, k, v,
+                                      head_stride, stream);
+}
+
+hga_status_t hga_attn_fwd_packed(const hga_params_t *p, const void *q, const void *hist, int hist_cap_chunks,
+                                 const void *k_seg, const void *v_seg, const int32_t *idx, void *out, float *lse,
+                                 cudaStream_t stream) {
+    CallRange range("hga_attn_fwd_packed");
+    hga_status_t st = check_params(p);
+    if (st != HGA_OK) return st;
+    if (p->q_block != 64) return HGA_ERR_UNSUPPORTED;  // one-token segments go through hga_attn_decode_packed
+    if (hist_cap_chunks < p->n_hist_chunks) return HGA_ERR_INVALID_ARG;
+    if (!q || !k_seg || !v_seg || !idx || !out || !lse) return HGA_ERR_INVALID_ARG;
+    if (p->n_hist_chunks > 0 && !hist) return HGA_ERR_INVALID_ARG;
+    for (const void *ptr : {q, hist, k_seg, v_seg, (const void *)out})
+        if (ptr && !aligned16(ptr)) return HGA_ERR_INVALID_ARG;
+    if (!hga::attn_fwd_tc_shape(*p)) {
+        hga::record_error("hga_attn_fwd_packed runs on the tcgen05 kernel only (bf16, head_dim 128)");
+        return HGA_ERR_UNSUPPORTED;
+    }
+    if (!hga::attn_fwd_packed_supported(*p)) {
+        hga::record_error("hga_attn_fwd_packed: the tcgen05 kernel cannot take this call (no TMA tensor-map "
+                          "encoder in the driver, or a row coordinate beyond 32 bits)");
+        return HGA_ERR_UNSUPPORTED;
+    }
+    unsigned *status = status_ptr();
+    if (!status) return hga::record_cuda(cudaErrorInvalidDevice);
+    return hga::launch_attn_fwd_packed(*p, q, static_cast<const uint8_t *>(hist), hist_cap_chunks, k_seg, v_seg, idx,
+                                       out, lse, status, stream);
+}
+
+hga_status_t hga_attn_decode_packed(const hga_params_t *p, const void *q, const void *hist, int hist_cap_chunks,
+                                    const void *k_local, const void *v_local, int n_local, const int32_t *idx,
+                                    void *out, float *lse, cudaStream_t stream) {
+    CallRange range("hga_attn_decode_packed");
+    hga_status_t st = check_params(p);
+    if (st != HGA_OK) return st;
+    if (p->seg_len != 1 || p->q_block != 1) return HGA_ERR_UNSUPPORTED;
+    if (n_local < 1 || p->seg_head_stride < n_local || hist_cap_chunks < p->n_hist_chunks) return HGA_ERR_INVALID_ARG;
+    if (p->dtype != HGA_BF16 || p->n_q_heads / p->n_kv_heads > 8) {
+        hga::record_error("hga_attn_decode_packed takes bf16 and at most 8 query heads per KV head");
+        return HGA_ERR_UNSUPPORTED;
+    }
+    if (!q || !k_local || !v_local || !idx || !out || !lse) return HGA_ERR_INVALID_ARG;
+    if (p->n_hist_chunks > 0 && !hist) return HGA_ERR_INVALID_ARG;
+    for (const void *ptr : {q, hist, k_local, v_local, (const void *)out})
+        if (ptr && !aligned16(ptr)) return HGA_ERR_INVALID_ARG;
+    // a cluster of up to 8 CTAs per (batch, KV head)
+    if ((long long)p->batch * p->n_kv_heads >= (1ll << 28)) return HGA_ERR_UNSUPPORTED;
+    unsigned *status = status_ptr();
+    if (!status) return hga::record_cuda(cudaErrorInvalidDevice);
+    return hga::launch_decode_packed(*p, q, static_cast<const uint8_t *>(hist), hist_cap_chunks, k_local, v_local,
+                                     n_local, idx, out, lse, status, stream);
+}
+
 hga_status_t hga_selftest_wait_timeout(long long wait_cycles, cudaStream_t stream) {
     CallRange range("hga_selftest_wait_timeout");
     if (wait_cycles < 1000 || wait_cycles > (1ll << 32)) return HGA_ERR_INVALID_ARG;

@@ -1,0 +1,590 @@
+// Exact-token attention forward over a packed history on the 5th-generation tensor cores
+// (tcgen05 / TMEM / TMA): bf16 queries and segment, 4-bit history (packed.cuh), fp32
+// accumulation, head_dim 128.
+//
+// "Long-Context Fine-Tuning with Limited VRAM", technical summary section 2.1 (exact K/V
+// of the routed chunks attended with a local window): what attn_fwd_tc.cu computes, with
+// the history's keys and values read as the values of their 4-bit records.
+//
+// One CTA per (batch, kv head, query block, head sub-group), as in attn_fwd_tc.cu: HC = 4,
+// 2 or 1 query heads of a KV group as NH M=128 halves share every 64-token tile.  The
+// records are widened inside the kernel, on four warps beside the ones that run the
+// softmax, so no bf16 copy of the history exists anywhere and a routed chunk costs 9 KiB
+// of HBM / L2 reads instead of 32.
+//
+// Warp roles (NH = 2: 512 threads):
+//   warps 0, 2  QK issuers of halves 0, 1 (warp 0 also owns TMEM):
+//               S_h = Q_h K^T  (M128 N64 K128, K-major A and B, SW128)
+//   warps 1, 3  PV issuers: O_h += P_h V  (M128 N128 K64, P from TMEM)
+//   then 4 NH   softmax warps: one TMEM lane (= query row) per thread, online softmax in
+//               the log2 domain, P written back as bf16 pairs into the tile's S buffer
+//   last 4      producers.  History tiles: each thread holds a tile's worth of codes and
+//               grids in registers (40 words, loaded one tile ahead), widens them and
+//               stores 16 bytes per word into the K / V stage: K as [2 column halves]
+//               [64 tokens][128 B], V transposed as [128 channels][128 B of tokens] --
+//               the record's own order, so one word is one swizzled 16-byte chunk in both
+//               -- hence V is K-major for these tiles.  Segment tiles: TMA, V as rows of
+//               tokens (MN-major); the PV issuers pick descriptor and instruction by tile.
+// A K (V) stage is full when all four producer warps have arrived; for a segment tile one
+// of them arrives with the byte count of its TMA boxes.
+// TMEM (512 columns): O_h at 128h, S_h double-buffered at 256 + 128h + 64b.
+// Every wait is bounded; a timeout sets HGA_DEV_TIMEOUT and the CTA unwinds.
+#include "packed.cuh"
+#include "tc_issue.cuh"
+#include "tc_ptx.cuh"
+
+namespace hga {
+
+namespace {
+
+constexpr int D = 128;
+constexpr int TILE = 64;
+constexpr int NSTAGE = 4;
+constexpr float kRescaleLog2 = 8.f;  // lazy-rescale threshold on the running max (log2 units)
+constexpr uint32_t Q_HALF_BYTES = 128 * D * 2;   // [2 col halves][128 rows][128 B]
+constexpr uint32_t KV_TILE_BYTES = TILE * D * 2; // K [2 col halves][64 rows][128 B]; V also [128 rows][128 B]
+constexpr uint32_t IDESC_QK = tc::idesc_bf16(128, TILE, false, false);
+constexpr uint32_t IDESC_PV = tc::idesc_bf16(128, D, false, true);        // segment: V rows are tokens
+constexpr uint32_t IDESC_PV_HIST = tc::idesc_bf16(128, D, false, false);  // history: V rows are channels
+constexpr int kIssueWarps = 4;
+constexpr int kProdWarps = 4;
+
+template <int NH> struct Smem {
+    static constexpr uint32_t Q = 0;
+    static constexpr uint32_t K = Q + NH * Q_HALF_BYTES;
+    static constexpr uint32_t V = K + NSTAGE * KV_TILE_BYTES;
+    static constexpr uint32_t BAR = V + NSTAGE * KV_TILE_BYTES;
+    static constexpr uint32_t TOTAL = BAR + 1024;
+    static constexpr uint32_t ALLOC = TOTAL + 1024;  // + alignment slack
+};
+
+// D[tmem] (+)= A[tmem] * B[smem] for one K=16 step of kind::f16 (A read from TMEM).
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+struct Bars {
+    uint64_t q_full;
+    uint64_t k_full[NSTAGE];
+    uint64_t k_empty[NSTAGE];  // released once QK^T of the tile completes (both halves)
+    uint64_t v_full[NSTAGE];
+    uint64_t v_empty[NSTAGE];  // released once PV of the tile completes (both halves)
+    uint64_t s_full[2][2];     // [half][S/P buffer]: S of the buffer's tile in TMEM
+    uint64_t p_full[2][2];     // [half][S/P buffer]: P of the buffer's tile written to TMEM
+    uint64_t o_done[2][2];     // [half][S/P buffer]: PV of the buffer's tile completed
+    uint64_t drain[4];         // one per issuing warp (abort path)
+    uint32_t tmem_base;
+    int abort;
+    int n_hist;
+    int sm0_tiles;  // tiles whose softmax half 0 has finished (scheduling hint)
+    int tiles[64];
+};
+static_assert(sizeof(Bars) <= 1024, "barrier block must fit its region");
+
+struct FwdPackedArgs {
+    int batch, n_q_heads, n_kv_heads, seg_len, topk, n_hist_chunks;
+    int n_sub, hc;  // CTAs per KV group, query heads per CTA (4, 2 or 1)
+    long long seg_stride, cap;
+    int qb0, n_blocks;
+    const uint8_t *hist;
+    const int32_t *idx;
+    __nv_bfloat16 *out;
+    float *lse;
+    unsigned *status;
+    float scale_log2;  // log2(e) / sqrt(D)
+};
+
+// Bounded wait until the shared counter reaches `target` (same contract as mbar_wait).
+__device__ __forceinline__ bool wait_count(int *counter, int target, volatile int *abort, unsigned *status) {
+    volatile int *c = counter;
+    if (*c >= target) return true;
+    const long long t0 = clock64();
+    while (*c < target) {
+        if (*abort) return false;
+        if (clock64() - t0 > (1ll << 31)) {
+            *abort = 1;
+            atomicOr(status, kDevTimeout);
+            return false;
+        }
+    }
+    return true;
+}
+
+// Codes and grid of one thread's share of a K part: octet `o` of the tokens r0 + 8 i.
+struct KShare {
+    uint32_t w[8], s[4], z[4];
+    __device__ __forceinline__ void load(const uint8_t *rec, int o, int r0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t *>(rec) + (r0 + 8 * i) * 16 + o);
+        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(rec + Packed<D>::kGridOff) + o);
+        const uint4 b = __ldg(reinterpret_cast<const uint4 *>(rec + Packed<D>::kGridOff + Packed<D>::kGridHalf) + o);
+        s[0] = a.x; s[1] = a.y; s[2] = a.z; s[3] = a.w;
+        z[0] = b.x; z[1] = b.y; z[2] = b.z; z[3] = b.w;
+    }
+};
+// The same of a V part: token octet `o` of the channels r0 + 16 i (i < 4: group 0).
+struct VShare {
+    uint32_t w[8], s[2][4], z[2][4];
+    __device__ __forceinline__ void load(const uint8_t *vrec, int o, int r0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t *>(vrec) + (r0 + 16 * i) * 8 + o);
+#pragma unroll
+        for (int gp = 0; gp < 2; ++gp) {
+            const uint8_t *grid = vrec + Packed<D>::kGridOff + gp * 2 * TILE;
+            const uint4 a = __ldg(reinterpret_cast<const uint4 *>(grid) + o);
+            const uint4 b = __ldg(reinterpret_cast<const uint4 *>(grid + Packed<D>::kGridHalf) + o);
+            s[gp][0] = a.x; s[gp][1] = a.y; s[gp][2] = a.z; s[gp][3] = a.w;
+            z[gp][0] = b.x; z[gp][1] = b.y; z[gp][2] = b.z; z[gp][3] = b.w;
+        }
+    }
+};
+
+template <int NH>
+__global__ void __launch_bounds__(32 * (kIssueWarps + 4 * NH + kProdWarps), 1)
+    attn_fwd_packed_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_ks,
+                           const __grid_constant__ CUtensorMap tm_vs, const FwdPackedArgs a) {
+    using L = Smem<NH>;
+    constexpr int kSoftmax0 = kIssueWarps, kProd0 = kIssueWarps + 4 * NH;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Bars *bars = reinterpret_cast<Bars *>(smem + L::BAR);
+    const uint32_t sbase = tc::smem_u32(smem);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int nqb = a.seg_len / TILE;
+    const int n_units = a.batch * a.n_kv_heads * a.n_sub;
+    const int m = a.qb0 + a.n_blocks - 1 - (int)blockIdx.x / n_units;  // longest (latest) blocks first
+    const int unit = (int)blockIdx.x % n_units;
+    const int bg = unit / a.n_sub;
+    const int b = bg / a.n_kv_heads, g = bg % a.n_kv_heads;
+    // first query head of this CTA: the KV group's heads g*G .., HC per CTA
+    const int h0 = g * (a.n_q_heads / a.n_kv_heads) + (unit % a.n_sub) * a.hc;
+
+    if (threadIdx.x == 0) {
+        tc::mbar_init(&bars->q_full, 1);
+        for (int s = 0; s < NSTAGE; ++s) {
+            tc::mbar_init(&bars->k_full[s], kProdWarps);
+            tc::mbar_init(&bars->k_empty[s], NH);
+            tc::mbar_init(&bars->v_full[s], kProdWarps);
+            tc::mbar_init(&bars->v_empty[s], NH);
+        }
+        for (int h = 0; h < 2; ++h)
+            for (int bb = 0; bb < 2; ++bb) {
+                tc::mbar_init(&bars->s_full[h][bb], 1);
+                tc::mbar_init(&bars->p_full[h][bb], 4);  // every softmax warp of the half
+                tc::mbar_init(&bars->o_done[h][bb], 1);
+            }
+        for (int d = 0; d < 4; ++d) tc::mbar_init(&bars->drain[d], 1);
+        bars->sm0_tiles = 0;
+        bars->abort = 0;
+        tc::fence_mbar_init();
+    }
+    if (warp == 1) {  // the block's valid routes, in order; -1 is padding, anything else is skipped and flagged
+        const int32_t *sel = a.idx + ((long long)bg * nqb + m) * a.topk;
+        int n = 0;
+#pragma unroll
+        for (int i0 = 0; i0 < 64; i0 += 32) {
+            const int j = i0 + lane < a.topk ? sel[i0 + lane] : -1;
+            const bool ok = j >= 0 && j < a.n_hist_chunks;
+            if (!ok && j != -1) atomicOr(a.status, kDevBadIndex);
+            const unsigned mask = __ballot_sync(0xffffffffu, ok);
+            if (ok) bars->tiles[n + __popc(mask & ((1u << lane) - 1u))] = j;
+            n += __popc(mask);
+        }
+        if (lane == 0) bars->n_hist = n;
+    }
+    if (warp == 0) tc::tmem_alloc<512>(&bars->tmem_base);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = bars->tmem_base;
+    volatile int *abort = &bars->abort;
+    const int n_hist = bars->n_hist;          // history tiles, then segment tiles 0 .. m
+    const int n_tiles = n_hist + m + 1;
+    int issued = 0;  // producer warp 0: tiles whose loads it has issued (drained on abort)
+
+    if (warp < kIssueWarps) {
+        // ------------------------------------------------------------ UMMA issuers
+        const int h = warp >> 1;           // M half
+        const bool qk = (warp & 1) == 0;   // warps 0, 2: QK^T; warps 1, 3: PV
+        if (h < NH) {
+            // The whole warp runs the loop (waits included) and elects one lane per MMA.
+            // Descriptors are built once; a K-step, stage or buffer offset is added
+            // to the start-address field (addresses stay below 2^18, so no carry).
+            bool ok = true;
+            if (qk) {
+                const uint64_t q_desc = tc::desc_sw128(sbase + L::Q + h * Q_HALF_BYTES, 16, 1024);
+                const uint64_t k_desc = tc::desc_sw128(sbase + L::K, 16, 1024);
+                ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars->q_full, 0, abort, a.status));
+                for (int j = 0; ok && j < n_tiles; ++j) {
+                    const int s = j % NSTAGE, bb = j & 1;
+                    if (!__all_sync(0xffffffffu, tc::mbar_wait(&bars->k_full[s], (j / NSTAGE) & 1, abort, a.status)))
+                        break;
+                    // S buffer bb is free once PV(j-2), which read P(j-2) from it, has completed
+                    if (j >= 2 && !__all_sync(0xffffffffu, tc::mbar_wait(&bars->o_done[h][bb], ((j >> 1) - 1) & 1,
+                                                                         abort, a.status)))
+                        break;
+                    // half 1 runs half a tile behind half 0, so that the two softmax groups
+                    // take turns on the MUFU
+                    if (h == 1 && j >= 1 && !__all_sync(0xffffffffu, wait_count(&bars->sm0_tiles, j, abort, a.status)))
+                        break;
+                    tc::fence_after_sync();
+                    const uint64_t kd = k_desc + (uint64_t)((s * KV_TILE_BYTES) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t koff = ((kk >> 2) * (64 * 128) + (kk & 3) * 32) >> 4;
+                        const uint32_t qoff = ((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4;
+                        if (tc::elect_one())
+                            tc::mma_f16(tmem + 256 + 128 * h + 64 * bb, q_desc + qoff, kd + koff, IDESC_QK,
+                                        kk > 0 ? 1u : 0u);
+                        __syncwarp();
+                    }
+                    if (tc::elect_one()) {
+                        tc::mma_commit(&bars->s_full[h][bb]);
+                        tc::mma_commit(&bars->k_empty[s]);  // one arrival per half
+                    }
+                    __syncwarp();
+                }
+            } else {
+                const uint64_t v_seg = tc::desc_sw128(sbase + L::V, 8192, 1024);  // rows of tokens
+                const uint64_t v_hist = tc::desc_sw128(sbase + L::V, 16, 1024);   // rows of channels
+                const uint32_t o_tmem = tmem + 128 * h;
+                for (int t = 0; t < n_tiles; ++t) {
+                    const int s = t % NSTAGE, pb = t & 1;
+                    if (!__all_sync(0xffffffffu, tc::mbar_wait(&bars->v_full[s], (t / NSTAGE) & 1, abort, a.status) &&
+                                                     tc::mbar_wait(&bars->p_full[h][pb], (t >> 1) & 1, abort,
+                                                                   a.status)))
+                        break;
+                    tc::fence_after_sync();
+                    const bool hist = t < n_hist;
+                    const uint64_t vd = (hist ? v_hist : v_seg) + (uint64_t)((s * KV_TILE_BYTES) >> 4);
+                    const uint32_t vstep = hist ? 32 >> 4 : 2048 >> 4;  // 16 tokens on
+                    const uint32_t idesc = hist ? IDESC_PV_HIST : IDESC_PV;
+                    // P(t) as bf16 pairs in the first 32 columns of S buffer pb: 8 columns per K step
+                    const uint32_t pa = tmem + 256 + 128 * h + 64 * pb;
+#pragma unroll
+                    for (int kk = 0; kk < TILE / 16; ++kk) {
+                        if (tc::elect_one())
+                            mma_f16_ts(o_tmem, pa + 8 * kk, vd + kk * vstep, idesc, (t > 0 || kk > 0) ? 1u : 0u);
+                        __syncwarp();
+                    }
+                    if (tc::elect_one()) {
+                        tc::mma_commit(&bars->o_done[h][pb]);
+                        tc::mma_commit(&bars->v_empty[s]);  // one arrival per half
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+    } else if (warp >= kProd0) {
+        // ------------------------------------------------------------ producers
+        const int t = (warp - kProd0) * 32 + lane;
+        const int ko = t & 15, kr = t >> 4;  // K: channel octet, first token
+        const int vo = t & 7, vr = t >> 3;   // V: token octet, first channel
+        // swizzle: a row's 16-byte chunk index is XORed with the row index mod 8, which
+        // is the same for all rows of a thread
+        const uint32_t kdst = sbase + L::K + (ko >> 3) * (64 * 128) + kr * 128 + (((ko & 7) ^ kr) << 4);
+        const uint32_t vdst = sbase + L::V + vr * 128 + ((vo ^ (vr & 7)) << 4);
+        const uint8_t *base = a.hist + (long long)bg * a.cap * Packed<D>::kRecord;
+        if (t == 0) {
+            tc::tma_prefetch_desc(&tm_q);
+            tc::tma_prefetch_desc(&tm_ks);
+            tc::tma_prefetch_desc(&tm_vs);
+            tc::mbar_arrive_expect_tx(&bars->q_full, NH * Q_HALF_BYTES);
+            for (int hh = 0; hh < 2 * NH; ++hh) {
+                const int qrow = (b * a.n_q_heads + h0 + (a.hc == 1 ? 0 : hh)) * a.seg_len + m * TILE;
+                uint8_t *dst = smem + L::Q + (hh >> 1) * Q_HALF_BYTES + (hh & 1) * (64 * 128);
+                tc::tma_load_2d(dst, &tm_q, 0, qrow, &bars->q_full);
+                tc::tma_load_2d(dst + 128 * 128, &tm_q, 64, qrow, &bars->q_full);
+            }
+        }
+        __syncwarp();
+        // a segment tile, or a warp's arrival for it
+        auto seg_tile = [&](uint8_t *dst, const CUtensorMap *map, int j, uint64_t *bar) {
+            if (t == 0) {
+                const int row = (int)((long long)bg * a.seg_stride + (long long)(j - n_hist) * TILE);
+                tc::mbar_arrive_expect_tx(bar, KV_TILE_BYTES);
+                tc::tma_load_2d(dst, map, 0, row, bar);
+                tc::tma_load_2d(dst + 64 * 128, map, 64, row, bar);
+            } else if (lane == 0) {
+                tc::mbar_arrive(bar);
+            }
+            __syncwarp();
+        };
+        // widened codes are visible to the tensor core before the warp arrives
+        auto publish = [&](uint64_t *bar) {
+            tc::fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(bar);
+        };
+        KShare ks;
+        VShare vs;
+        if (n_hist > 0) {
+            const uint8_t *rec = base + (long long)bars->tiles[0] * Packed<D>::kRecord;
+            ks.load(rec, ko, kr);
+            vs.load(rec + Packed<D>::kPart, vo, vr);
+        }
+        for (int j = 0; j < n_tiles; ++j) {
+            const int s = j % NSTAGE, u = j / NSTAGE;
+            const uint8_t *next =
+                j + 1 < n_hist ? base + (long long)bars->tiles[j + 1] * Packed<D>::kRecord : nullptr;
+            // a stage frees once the products of the tile NSTAGE back have read it
+            if (j >= NSTAGE &&
+                !__all_sync(0xffffffffu, tc::mbar_wait(&bars->k_empty[s], (u - 1) & 1, abort, a.status)))
+                break;
+            if (j < n_hist) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    uint32_t r[4];
+                    packed_octet(ks.w[i], ks.s, ks.z, r);
+                    tc::st_shared_v4(kdst + s * KV_TILE_BYTES + i * 8 * 128, r[0], r[1], r[2], r[3]);
+                }
+                publish(&bars->k_full[s]);
+                if (next) ks.load(next, ko, kr);
+            } else {
+                seg_tile(smem + L::K + s * KV_TILE_BYTES, &tm_ks, j, &bars->k_full[s]);
+            }
+            issued = 2 * j + 1;
+            if (j >= NSTAGE &&
+                !__all_sync(0xffffffffu, tc::mbar_wait(&bars->v_empty[s], (u - 1) & 1, abort, a.status)))
+                break;
+            if (j < n_hist) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    uint32_t r[4];
+                    packed_octet(vs.w[i], vs.s[i >> 2], vs.z[i >> 2], r);
+                    tc::st_shared_v4(vdst + s * KV_TILE_BYTES + i * 16 * 128, r[0], r[1], r[2], r[3]);
+                }
+                publish(&bars->v_full[s]);
+                if (next) vs.load(next + Packed<D>::kPart, vo, vr);
+            } else {
+                seg_tile(smem + L::V + s * KV_TILE_BYTES, &tm_vs, j, &bars->v_full[s]);
+            }
+            issued = 2 * j + 2;
+        }
+    } else {
+        // -------------------------------------------------------------- softmax / epilogue
+        const int h = (warp - kSoftmax0) >> 2;  // M half
+        const int quad = warp & 3;               // TMEM lane quadrant this warp may access
+        const int r = quad * 32 + lane;          // row within the half = TMEM lane
+        const int hh = 2 * h + (r >> 6);         // head within the group
+        const int i = r & 63;                    // query row within the block
+        const uint32_t lane_addr = (uint32_t)(quad * 32) << 16;
+        const uint32_t o_addr = tmem + lane_addr + 128 * h;
+        float m_run = -INFINITY, l_run = 0.f;
+        bool ok = true;
+        for (int j = 0; j < n_tiles; ++j) {
+            const int bb = j & 1;
+            // tcgen05.ld/st below are warp-collective: keep every decision warp-uniform
+            if (!__all_sync(0xffffffffu, tc::mbar_wait(&bars->s_full[h][bb], (j >> 1) & 1, abort, a.status))) {
+                ok = false;
+                break;
+            }
+            tc::fence_after_sync();
+            uint32_t sr[64];
+            {
+                uint32_t (&lo)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[0]);
+                uint32_t (&hi)[32] = *reinterpret_cast<uint32_t(*)[32]>(&sr[32]);
+                const uint32_t s_addr = tmem + lane_addr + 256 + 128 * h + 64 * bb;
+                tc::tmem_ld32(s_addr, lo);
+                tc::tmem_ld32(s_addr + 32, hi);
+                tc::tmem_wait_ld();
+            }
+            float x[64];
+            const bool diag = (j == n_tiles - 1);  // the local tile of this block (warp-uniform)
+#pragma unroll
+            for (int c = 0; c < 64; ++c) x[c] = __uint_as_float(sr[c]);
+            if (diag) {
+#pragma unroll
+                for (int c = 0; c < 64; ++c)
+                    if (c > i) x[c] = -INFINITY;
+            }
+            // row max of the raw scores (the scale is positive), 8 independent chains
+            float mpart[8];
+#pragma unroll
+            for (int c = 0; c < 64; ++c) mpart[c & 7] = (c < 8) ? x[c] : fmaxf(mpart[c & 7], x[c]);
+            const float mx = fmaxf(fmaxf(fmaxf(mpart[0], mpart[1]), fmaxf(mpart[2], mpart[3])),
+                                   fmaxf(fmaxf(mpart[4], mpart[5]), fmaxf(mpart[6], mpart[7]))) *
+                             a.scale_log2;
+            // Lazy rescaling: the reference max only moves when the row max grows by
+            // more than kRescaleLog2, so P stays <= 2^kRescaleLog2 and O is rescaled
+            // in TMEM only on those (rare) tiles.
+            const bool grow = mx > m_run + kRescaleLog2;
+            const float m_use = grow ? mx : m_run;
+            const float alpha = grow ? tc::ex2(m_run - m_use) : 1.f;
+            // a row with no unmasked key yet keeps m = -inf; its p must come out 0, not NaN
+            const float m_sub = m_use == -INFINITY ? 0.f : m_use;
+            float spart[8];
+#pragma unroll
+            for (int c = 0; c < 64; ++c) {
+                // p = 2^(s * log2(e)/sqrt(D) - m)
+                x[c] = tc::ex2(fmaf(x[c], a.scale_log2, -m_sub));
+                spart[c & 7] = (c < 8) ? x[c] : spart[c & 7] + x[c];
+            }
+            const float sum = ((spart[0] + spart[1]) + (spart[2] + spart[3])) +
+                              ((spart[4] + spart[5]) + (spart[6] + spart[7]));
+            l_run = l_run * alpha + sum;
+            const int pb = j & 1;
+            // a rescale needs O complete up to tile j-1 (PV(j-1) done) before PV(j) adds to it;
+            // rows that keep their reference max have alpha == 1, an exact no-op
+            if (j >= 1 && __any_sync(0xffffffffu, grow)) {
+                if (!__all_sync(0xffffffffu, tc::mbar_wait(&bars->o_done[h][pb ^ 1], ((j - 1) >> 1) & 1, abort,
+                                                            a.status))) {
+                    ok = false;
+                    break;
+                }
+                tc::fence_after_sync();
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    uint32_t o[32];
+                    tc::tmem_ld32(o_addr + c0, o);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+                    tc::tmem_st32(o_addr + c0, o);
+                }
+                tc::tmem_wait_st();
+            }
+            m_run = m_use;
+            // P as bf16 pairs over the first 32 columns of this tile's S buffer (already
+            // read into registers); PV reads it from there as its A operand
+            {
+                uint32_t pk[32];
+#pragma unroll
+                for (int c = 0; c < 32; ++c) pk[c] = tc::pack_bf16(x[2 * c], x[2 * c + 1]);
+                tc::tmem_st32(tmem + lane_addr + 256 + 128 * h + 64 * pb, pk);
+                tc::tmem_wait_st();
+            }
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bars->p_full[h][pb]);
+            if (NH == 2 && warp == kSoftmax0 && lane == 0) *reinterpret_cast<volatile int *>(&bars->sm0_tiles) = j + 1;
+        }
+        if (ok && __all_sync(0xffffffffu, tc::mbar_wait(&bars->o_done[h][(n_tiles - 1) & 1],
+                                                        ((n_tiles - 1) >> 1) & 1, abort, a.status))) {
+            tc::fence_after_sync();
+            const bool write = hh < a.hc;  // rows 64..127 repeat the head when HC = 1
+            const long long row = ((long long)(b * a.n_q_heads + h0 + (write ? hh : 0))) * a.seg_len + m * TILE + i;
+            __nv_bfloat16 *orow = a.out + row * D;
+            const float inv_l = 1.f / l_run;
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 32) {
+                uint32_t o[32];
+                tc::tmem_ld32(o_addr + c0, o);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 32; c += 8) {
+                    if (!write) break;
+                    uint4 v;
+                    v.x = tc::pack_bf16(__uint_as_float(o[c + 0]) * inv_l, __uint_as_float(o[c + 1]) * inv_l);
+                    v.y = tc::pack_bf16(__uint_as_float(o[c + 2]) * inv_l, __uint_as_float(o[c + 3]) * inv_l);
+                    v.z = tc::pack_bf16(__uint_as_float(o[c + 4]) * inv_l, __uint_as_float(o[c + 5]) * inv_l);
+                    v.w = tc::pack_bf16(__uint_as_float(o[c + 6]) * inv_l, __uint_as_float(o[c + 7]) * inv_l);
+                    *reinterpret_cast<uint4 *>(orow + c0 + c) = v;
+                }
+            }
+            if (write) a.lse[row] = (m_run + __log2f(l_run)) * 0.69314718055994530942f;
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (*abort) {
+        // a wait gave up: let the copies and UMMAs still in flight finish before
+        // shared memory and TMEM are released
+        int never = 0;
+        if (warp == kProd0 && lane == 0) {
+            // stages whose segment tiles this thread loaded last (K tiles 0 .. nk - 1, V
+            // tiles 0 .. nv - 1); their barriers complete once the other producer warps
+            // have arrived too, which an aborting one may not have: the wait is bounded
+            const int nk = (issued + 1) / 2, nv = issued / 2;
+            for (int j = nk - NSTAGE < n_hist ? n_hist : nk - NSTAGE; j < nk; ++j)
+                tc::mbar_wait(&bars->k_full[j % NSTAGE], (j / NSTAGE) & 1, &never, a.status, 1ll << 28);
+            for (int j = nv - NSTAGE < n_hist ? n_hist : nv - NSTAGE; j < nv; ++j)
+                tc::mbar_wait(&bars->v_full[j % NSTAGE], (j / NSTAGE) & 1, &never, a.status, 1ll << 28);
+            tc::mbar_wait(&bars->q_full, 0, &never, a.status, 1ll << 28);
+        }
+        if (warp < kIssueWarps && (warp >> 1) < NH) {
+            // the lane that issued this warp's MMAs commits and waits for them
+            if (tc::elect_one()) {
+                tc::mma_commit(&bars->drain[warp]);
+                tc::mbar_wait(&bars->drain[warp], 0, &never, a.status, 1ll << 28);
+            }
+        }
+        __syncwarp();
+        tc::fence_after_sync();
+        __syncthreads();
+    }
+    if (warp == 0) {
+        __syncwarp();
+        tc::tmem_dealloc<512>(tmem);
+    }
+}
+
+template <int NH>
+hga_status_t launch_nh(const hga_params_t &p, const void *q, const uint8_t *hist, int cap, const void *ks,
+                       const void *vs, const int32_t *idx, void *out, float *lse, unsigned *status,
+                       cudaStream_t stream) {
+    CUtensorMap mq, mks, mvs;
+    const long long n_bg = (long long)p.batch * p.n_kv_heads;
+    const unsigned long long seg_rows = (unsigned long long)((n_bg - 1) * p.seg_head_stride + p.seg_len);
+    if (!tma_rows_map(&mq, q, (unsigned long long)p.batch * p.n_q_heads * p.seg_len) ||
+        !tma_rows_map(&mks, ks, seg_rows) || !tma_rows_map(&mvs, vs, seg_rows)) {
+        record_error("hga_attn_fwd_packed: TMA tensor map encoding failed");
+        return HGA_ERR_UNSUPPORTED;
+    }
+    const int nqb = p.seg_len / p.q_block;
+    const int G = p.n_q_heads / p.n_kv_heads;
+    FwdPackedArgs a;
+    a.hc = NH == 2 ? 4 : (G % 2 == 0 ? 2 : 1);
+    a.n_sub = G / a.hc;
+    a.batch = p.batch;
+    a.n_q_heads = p.n_q_heads;
+    a.n_kv_heads = p.n_kv_heads;
+    a.seg_len = p.seg_len;
+    a.topk = p.topk;
+    a.n_hist_chunks = p.n_hist_chunks;
+    a.seg_stride = p.seg_head_stride;
+    a.cap = cap;
+    a.qb0 = p.qblock_end > 0 ? p.qblock_begin : 0;
+    a.n_blocks = (p.qblock_end > 0 ? p.qblock_end : nqb) - a.qb0;
+    a.hist = hist;
+    a.idx = idx;
+    a.out = static_cast<__nv_bfloat16 *>(out);
+    a.lse = lse;
+    a.status = status;
+    a.scale_log2 = (float)(1.4426950408889634 / __builtin_sqrt((double)D));
+    auto kern = attn_fwd_packed_kernel<NH>;
+    cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kern), (int)Smem<NH>::ALLOC);
+    if (e != cudaSuccess) return record_cuda(e);
+    const unsigned grid = (unsigned)(a.n_blocks * n_bg * a.n_sub);
+    kern<<<grid, 32 * (kIssueWarps + 4 * NH + kProdWarps), Smem<NH>::ALLOC, stream>>>(mq, mks, mvs, a);
+    return record_cuda(cudaGetLastError());
+}
+
+}  // namespace
+
+bool attn_fwd_packed_supported(const hga_params_t &p) {
+    if (!attn_fwd_tc_shape(p)) return false;
+    // TMA row coordinates are 32-bit (queries and segment; the history is not read by TMA)
+    if ((long long)p.batch * p.n_kv_heads * p.seg_head_stride >= (1ll << 31) ||
+        (long long)p.batch * p.n_q_heads * p.seg_len >= (1ll << 31))
+        return false;
+    return tma_encoder_available();
+}
+
+hga_status_t launch_attn_fwd_packed(const hga_params_t &p, const void *q, const uint8_t *hist, int cap,
+                                    const void *ks, const void *vs, const int32_t *idx, void *out, float *lse,
+                                    unsigned *status, cudaStream_t stream) {
+    if (p.n_q_heads / p.n_kv_heads % 4 == 0)
+        return launch_nh<2>(p, q, hist, cap, ks, vs, idx, out, lse, status, stream);
+    return launch_nh<1>(p, q, hist, cap, ks, vs, idx, out, lse, status, stream);
+}
+
+}  // namespace hga

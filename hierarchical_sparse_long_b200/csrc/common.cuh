@@ -161,6 +161,21 @@ hga_status_t launch_qk_norm_rope_bwd(const hga_proj_t &p, const void *q, const v
                                      const float *dq, const float *dk, const float *dv, void *dq_in, void *dk_in,
                                      void *dv_in, float *dqw, float *dkw, float *ws, unsigned *status,
                                      cudaStream_t stream);
+// Packed (4-bit) history: packed_history.cu, decode_packed.cu, attn_fwd_packed_tc.cu.
+hga_status_t launch_pack_history(const void *k, const void *v, long long head_stride, long long slices, int head_dim,
+                                 int first_chunk, int n_chunks, hga_dtype_t dtype, uint8_t *hist, int cap, float *summ,
+                                 int summ_cap, cudaStream_t stream);
+hga_status_t launch_unpack_history(const uint8_t *hist, int cap, long long slices, int head_dim, int first_chunk,
+                                   int n_chunks, hga_dtype_t dtype, void *k, void *v, long long head_stride,
+                                   cudaStream_t stream);
+// attn_fwd_tc_shape, the TMA encoder is available and the segment's row coordinates fit 32 bits.
+bool attn_fwd_packed_supported(const hga_params_t &p);
+hga_status_t launch_attn_fwd_packed(const hga_params_t &p, const void *q, const uint8_t *hist, int cap,
+                                    const void *ks, const void *vs, const int32_t *idx, void *out, float *lse,
+                                    unsigned *status, cudaStream_t stream);
+hga_status_t launch_decode_packed(const hga_params_t &p, const void *q, const uint8_t *hist, int cap, const void *kl,
+                                  const void *vl, int n_local, const int32_t *idx, void *out, float *lse,
+                                  unsigned *status, cudaStream_t stream);
 hga_status_t launch_selftest_wait_timeout(long long wait_cycles, unsigned *status, cudaStream_t stream);
 hga_status_t record_cuda(cudaError_t e);
 void record_error(const char *msg);

@@ -110,6 +110,11 @@ __device__ __forceinline__ uint4 ld_dsmem_v4(uint32_t addr) {
                  : "memory");
     return v;
 }
+__device__ __forceinline__ float ld_dsmem_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
 // Every thread of every CTA of the cluster arrives / waits (release / acquire).
 __device__ __forceinline__ void cluster_arrive() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");

@@ -615,6 +615,70 @@ hga_status_t hga_qk_norm_rope_bwd(const hga_proj_t *p, const void *q, const void
                                   void *dq_in, void *dk_in, void *dv_in, float *dq_weight, float *dk_weight,
                                   void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
+/* Packed history: detached chunks held in 4 bits (technical summary section 2.2:
+ * detached K/V are only read, and device memory bounds the context; the pages do
+ * not describe this form).  A record is the K and V of one chunk of one KV head,
+ * hga_packed_chunk_bytes(D) = 72 D bytes (bf16: 256 D), in this order:
+ *   K codes  uint32 [64 tokens][D/8]: word w of a token holds channels 8w .. 8w + 7
+ *   K grid   bf16 s[D], z[D]: a pair per channel
+ *   V codes  uint32 [D channels][8]: word w of a channel holds tokens 8w .. 8w + 7
+ *   V grid   bf16 s[D/64][64], z[D/64][64]: a pair per 64 channels and token
+ * Nibble j < 4 of a word is its element 2j, nibble 4 + j its element 2j + 1.  Code c
+ * stands for bf16(s (16 + c) + z), rounded once.  For a group (one pair's elements)
+ * with extremes mn, mx:
+ *   s = bf16(fl32(fl32(mx - mn) / 15)), 0 if below 2^-100;  z = bf16(fl32(mn - 16 s));
+ *   c = the code nearest to the element, (x - z) / s - 16 rounded to even in 0 .. 15.
+ * So a value is off by at most half a step s/2, the roundings of z and of the value
+ * (2^-9 |z| and 2^-9 |value|) and, at the ends, the range that rounding s lost.  A group
+ * whose sum is not finite (a NaN or an infinity in it) reads back as NaN.
+ *   hist: device, 16-byte aligned, [B][Hkv][hist_cap_chunks] records.
+ * The attention calls below attend exactly the values that hga_unpack_history
+ * returns; a backward pass (or any other call of this header) over packed history
+ * unpacks the chunks it needs first. */
+size_t hga_packed_chunk_bytes(int head_dim);
+
+/* Packs chunks [first_chunk, first_chunk + n_chunks) of every (b, g) into their
+ * records: the detach of a closed segment or window.
+ *   k, v: device, dtype, [B][Hkv][head_stride][D]; row 0 of each slice is the first
+ *     token of chunk first_chunk (head_stride >= n_chunks * 64).
+ *   summ: may be null; else the chunks' summaries are appended too, from the same
+ *     read of k and bit-identical to hga_build_summaries (layout as there,
+ *     first_chunk + n_chunks <= summ_cap_chunks).
+ * Records of other chunks are left as they were.  n_chunks == 0 is a no-op. */
+hga_status_t hga_pack_history(const void *k, const void *v, long long head_stride, int batch, int n_kv_heads,
+                              int head_dim, int first_chunk, int n_chunks, hga_dtype_t dtype, void *hist,
+                              int hist_cap_chunks, float *summ, int summ_cap_chunks, cudaStream_t stream);
+
+/* The values of chunks [first_chunk, first_chunk + n_chunks) of every (b, g), to
+ * rows [0, n_chunks * 64) of the slices of k and v (device, dtype; the values are
+ * bf16 numbers in either).  n_chunks == 0 is a no-op. */
+hga_status_t hga_unpack_history(const void *hist, int hist_cap_chunks, int batch, int n_kv_heads, int head_dim,
+                                int first_chunk, int n_chunks, hga_dtype_t dtype, void *k, void *v,
+                                long long head_stride, cudaStream_t stream);
+
+/* hga_attn_fwd over a packed history: history chunk j of head (b, g) is its record's
+ * values; queries, segment and outputs as there.
+ *   p: as for hga_attn_fwd (hist_head_stride is not used); bf16 with head_dim 128
+ *     only, on the tcgen05 kernel (else HGA_ERR_UNSUPPORTED).
+ *   hist: hist_cap_chunks >= n_hist_chunks records per (b, g); may be null when
+ *     n_hist_chunks is 0.
+ * The V rows of a block's own 64-token segment tile are all multiplied, those after
+ * a query with weight zero, so they must be finite (as in hga_attn_fwd).  Route
+ * indices outside [-1, Nc) are skipped and flagged HGA_DEV_BAD_INDEX. */
+hga_status_t hga_attn_fwd_packed(const hga_params_t *p, const void *q, const void *hist, int hist_cap_chunks,
+                                 const void *k_seg, const void *v_seg, const int32_t *idx, void *out, float *lse,
+                                 cudaStream_t stream);
+
+/* hga_attn_decode over a packed history, the local window in bf16: one new token per
+ * sequence attends the values of its routed chunks' records and its n_local window
+ * tokens.  One kernel, no workspace.
+ *   p: seg_len = q_block = 1, bf16, n_q_heads / n_kv_heads <= 8; seg_head_stride as
+ *     for hga_attn_decode, hist_head_stride not used.  hist as above.  Other arguments
+ *     as for hga_attn_decode; rows of the window past n_local are not read. */
+hga_status_t hga_attn_decode_packed(const hga_params_t *p, const void *q, const void *hist, int hist_cap_chunks,
+                                    const void *k_local, const void *v_local, int n_local, const int32_t *idx,
+                                    void *out, float *lse, cudaStream_t stream);
+
 /* Self-test of the bounded waits (the source pages have no counterpart): every
  * pipeline wait in the tensor-core kernels gives up after a cycle limit instead
  * of hanging, sets HGA_DEV_TIMEOUT and lets the kernel end.  This launches one

@@ -56,7 +56,9 @@ def to_bf16(x):
 
 
 def bf16_bits(x):
-    return (np.asarray(x, dtype=np.float32).view(np.uint32) >> 16).astype(np.uint16)
+    """Bits of bf16 values; a NaN is 0x7FFF, as CUDA's conversion writes it."""
+    x = np.asarray(x, dtype=np.float32)
+    return np.where(np.isnan(x), 0x7FFF, x.view(np.uint32) >> 16).astype(np.uint16)
 
 
 def quant(x, axis):
@@ -104,3 +106,27 @@ def pack(k, v):
     parts += [_bytes(_words(ct), lead), _bytes(bf16_bits(s[..., 0].swapaxes(3, 4)), lead),
               _bytes(bf16_bits(z[..., 0].swapaxes(3, 4)), lead)]
     return np.concatenate(parts, axis=-1), kv, vv
+
+
+# ------------------------------------------------------------------ attention
+def attend(q, keys, vals, mask):
+    """q [R][D], keys / vals [T][D], mask [R or 1][T] (float64): out, lse, the magnitude
+    sum_t p_t |v_t| of every output, and the largest sum_i |q_i k_i| / sqrt(D) of a row."""
+    scale = q.shape[-1] ** -0.5
+    x = np.where(mask, (q @ keys.T) * scale, -np.inf)
+    top = x.max(-1, keepdims=True)
+    p = np.exp(x - top)
+    l = p.sum(-1, keepdims=True)
+    p /= l
+    size = np.where(mask, (abs(q) @ abs(keys).T) * scale, 0.0).max(-1, keepdims=True)
+    return p @ vals, (top + np.log(l))[..., 0], p @ abs(vals), size
+
+
+def attend_tol(out, mag, size, d, n):
+    """Bounds of bf16 attention over n tokens with fp32 sums.  A score is d products and sums
+    whose additions may truncate (2 u each) and a scaling, its exponential has the same
+    absolute error and 4 u of its own; the row sum and the products over P add n truncating
+    sums; P and the output are rounded to bf16."""
+    score = (2 * d + 8) * U32 * size
+    rel = 2 * score + (4 * n + 64) * U32
+    return HALF["bf16"] * abs(out) + (HALF["bf16"] + rel) * mag, rel[..., 0]

@@ -1,0 +1,465 @@
+"""GPU parity of the 4-bit packed history against its definition in 64 bits: records bit for
+bit, attention over the values that the records stand for within the bounds of
+packed_ref.attend_tol."""
+import numpy as np
+import pytest
+import torch
+
+from tests import hga_cases as hc
+from tests import packed_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+BF16 = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    hc.ensure_built()
+    assert torch.cuda.is_available()
+    yield
+    import hierarchical_sparse_long_b200 as hga
+    assert hga.hga_get_device_status() == 0
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def host(a, dtype=BF16):
+    """A host array's values in dtype, on the device."""
+    return torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).cuda().to(dtype)
+
+
+def keys(rng, *shape):
+    """Keys with an offset per slice of 64 tokens and two strong channels."""
+    x = rng.standard_normal(shape)
+    x[..., 3] += 6.0
+    x[..., 17] *= 5.0
+    return x
+
+
+# ------------------------------------------------------------------ records
+# (B, Hkv, D, dtype, first chunk, chunks, cap, head stride beyond the chunks)
+PACK = [
+    (1, 1, 64, "bf16", 0, 1, 1, 0),
+    (1, 1, 128, "fp32", 0, 1, 3, 0),
+    (2, 3, 128, "bf16", 2, 5, 9, 37),
+    (3, 2, 64, "fp32", 1, 3, 4, 1),
+    (1, 5, 64, "bf16", 4, 7, 11, 128),
+    (1, 8, 128, "bf16", 0, 40, 41, 0),
+]
+
+
+@pytest.mark.parametrize("case", PACK, ids=str)
+def test_records_are_the_definition_bit_for_bit(case):
+    import hierarchical_sparse_long_b200 as hga
+    B, H, D, dtype, first, n, cap, extra = case
+    rng = np.random.default_rng(sum(case[:3]) + n)
+    dt = BF16 if dtype == "bf16" else torch.float32
+    stride = n * 64 + extra
+    k, v = host(keys(rng, B, H, stride, D), dt), host(rng.standard_normal((B, H, stride, D)), dt)
+    hist = torch.full((B, H, cap, hga.hga_packed_chunk_bytes(D)), 0xA5, device="cuda", dtype=torch.uint8)
+    summ = torch.full((B, H, cap, D), 7.0, device="cuda")
+    hga.hga_pack_history(k, v, stride, B, H, D, first, n, hist, cap, summ, cap)
+    rec, kv, vv = ref.pack(f64(k)[:, :, :n * 64], f64(v)[:, :, :n * 64])
+    got = hist.cpu().numpy()
+    assert np.array_equal(got[:, :, first:first + n], rec)
+    assert np.all(got[:, :, :first] == 0xA5) and np.all(got[:, :, first + n:] == 0xA5)
+    want = torch.full_like(summ, 7.0)
+    chunk0 = torch.empty(B, H, n, D, device="cuda")
+    hga.hga_build_summaries(k, stride, B, H, D, 64, 0, n, chunk0, n)
+    want[:, :, first:first + n] = chunk0
+    assert torch.equal(summ, want)
+    # and back, to either type, rows behind the chunks left as they were
+    for out in (BF16, torch.float32):
+        k2 = torch.full((B, H, stride, D), 7.0, device="cuda", dtype=out)
+        v2 = torch.full_like(k2, 7.0)
+        hga.hga_unpack_history(hist, cap, B, H, D, first, n, k2, v2, stride)
+        for t, x in ((k2, kv), (v2, vv)):
+            assert np.array_equal(f64(t)[:, :, :n * 64], x)
+            assert torch.all(t[:, :, n * 64:] == 7.0)
+
+
+def test_without_summaries_and_no_chunks():
+    import hierarchical_sparse_long_b200 as hga
+    rng = np.random.default_rng(3)
+    k, v = host(keys(rng, 1, 2, 128, 64)), host(rng.standard_normal((1, 2, 128, 64)))
+    hist = torch.zeros(1, 2, 2, 72 * 64, device="cuda", dtype=torch.uint8)
+    hga.hga_pack_history(k, v, 128, 1, 2, 64, 0, 2, hist, 2)
+    assert np.array_equal(hist.cpu().numpy(), ref.pack(f64(k), f64(v))[0])
+    before = hist.clone()
+    hga.hga_pack_history(k, v, 128, 1, 2, 64, 2, 0, hist, 2)
+    hga.hga_unpack_history(hist, 2, 1, 2, 64, 0, 0, k, v, 128)
+    assert torch.equal(hist, before)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_extreme_groups(D, dtype):
+    """Constant, tiny, huge and non-finite groups, and values on the borders between codes."""
+    import hierarchical_sparse_long_b200 as hga
+    rng = np.random.default_rng(D)
+    dt = BF16 if dtype == "bf16" else torch.float32
+    n = 5
+    k, v = keys(rng, 1, 1, n * 64, D), rng.standard_normal((1, 1, n * 64, D))
+    k[..., 0] = 1.5                                     # no range: read back as they are
+    k[..., 1] = 2.0 ** -110 * rng.standard_normal(n * 64)  # a range below the smallest step
+    k[..., 2] = 1e30 * rng.standard_normal(n * 64)
+    k[..., 4] = np.arange(n * 64) % 16                  # the grid's own points
+    k[..., 5] = np.arange(n * 64) % 31 / 2              # and halfway between
+    k[..., 6] = 1000 + 0.01 * rng.standard_normal(n * 64)
+    k[:, :, 7, 7] = np.nan
+    k[:, :, 70, 8] = np.inf
+    k[:, :, 130, 9], k[:, :, 131, 9] = np.inf, -np.inf
+    v[:, :, 5] = -0.75
+    v[:, :, 6] = np.arange(D) % 16
+    v[:, :, 7] = np.arange(D) % 31 / 2
+    v[:, :, 9, 33] = np.nan
+    v[:, :, 10, 2] = -np.inf
+    v[:, :, 11] *= 1e30
+    v[:, :, 12] *= 2.0 ** -110
+    k, v = host(k, dt), host(v, dt)
+    hist = torch.zeros(1, 1, n, 72 * D, device="cuda", dtype=torch.uint8)
+    hga.hga_pack_history(k, v, n * 64, 1, 1, D, 0, n, hist, n)
+    rec, kv, vv = ref.pack(f64(k), f64(v))
+    assert np.array_equal(hist.cpu().numpy(), rec)
+    k2, v2 = torch.empty_like(k), torch.empty_like(v)
+    hga.hga_unpack_history(hist, n, 1, 1, D, 0, n, k2, v2, n * 64)
+    assert np.array_equal(f64(k2), kv, equal_nan=True) and np.array_equal(f64(v2), vv, equal_nan=True)
+    assert np.all(np.isnan(f64(k2)[0, 0, :64, 7])) and np.all(f64(k2)[0, 0, :, 0] == 1.5)
+    g = 32 // 64 * 64
+    assert np.all(np.isnan(f64(v2)[0, 0, 9, g:g + 64]))
+    # the documented bound of a finite group: half a step, the roundings of z and of the
+    # value, and the range that rounding s lost (15 steps of 2^-8, over at most both ends)
+    for t, t2, axis in ((f64(k).reshape(n, 64, D), f64(k2).reshape(n, 64, D), 1),
+                        (f64(v).reshape(n * 64, D // 64, 64), f64(v2).reshape(n * 64, D // 64, 64), 2)):
+        s, z, _ = ref.quant(t, axis)
+        with np.errstate(invalid="ignore"):
+            bound = 0.5 * s + 2.0 ** -8 * abs(z) + 2.0 ** -8 * abs(t2) + 15 * 2.0 ** -8 * s + (s == 0) * 2.0 ** -96
+            assert np.all((abs(t - t2) <= bound) | ~np.isfinite(s))
+
+
+# ------------------------------------------------------------------ attention
+class Packed:
+    """A packed history of random chunks, its values in 64 bits and a bf16 window or segment."""
+
+    def __init__(self, B, Hq, Hkv, D, topk, nc, n_seg, blocks, seed=0, cap_extra=2, stride_extra=5, routes="random"):
+        import hierarchical_sparse_long_b200 as hga
+        rng = np.random.default_rng(7 * seed + B + Hq + nc + topk)
+        self.shape = (B, Hq, Hkv, D, topk, nc)
+        self.cap = nc + cap_extra
+        self.stride = n_seg + stride_extra
+        self.n_seg, self.blocks = n_seg, blocks
+        self.hist = torch.full((B, Hkv, self.cap, 72 * D), 0xFF, device="cuda", dtype=torch.uint8)
+        kh, vh = host(keys(rng, B, Hkv, nc * 64, D)), host(rng.standard_normal((B, Hkv, nc * 64, D)))
+        if nc:
+            hga.hga_pack_history(kh, vh, nc * 64, B, Hkv, D, 0, nc, self.hist, self.cap)
+            _, self.kh, self.vh = ref.pack(f64(kh), f64(vh))
+        rows = 64 * blocks if n_seg == 64 * blocks else 1
+        self.rows = rows
+        self.q = host(rng.standard_normal((B, Hq, rows, D)))
+        self.k = torch.full((B, Hkv, self.stride, D), float("nan"), device="cuda", dtype=BF16)
+        self.v = torch.full_like(self.k, float("nan"))
+        self.k[:, :, :n_seg] = host(keys(rng, B, Hkv, n_seg, D))
+        self.v[:, :, :n_seg] = host(rng.standard_normal((B, Hkv, n_seg, D)))
+        idx = np.full((B, Hkv, blocks, topk), -1, dtype=np.int32)
+        for at in np.ndindex(B, Hkv, blocks):
+            n = min(topk, nc)
+            idx[at][:n] = np.sort(rng.permutation(nc)[:n])
+            if routes == "holes":
+                idx[at][rng.permutation(topk)[:topk // 2]] = -1
+            if routes == "none":
+                idx[at] = -1
+            if routes == "twice" and n > 1:
+                idx[at][1] = idx[at][0]
+        self.idx_host, self.idx = idx, torch.from_numpy(idx).cuda()
+        self.out = torch.full((B, Hq, rows, D), 7.0, device="cuda", dtype=BF16)
+        self.lse = torch.full((B, Hq, rows), 7.0, device="cuda")
+        self.p = hga.Params(B, Hq, Hkv, D, topk, rows, nc, seg_head_stride=self.stride, q_block=64 if rows > 1 else 1)
+
+    def run(self, stream=None, out=None, lse=None):
+        import hierarchical_sparse_long_b200 as hga
+        out, lse = self.out if out is None else out, self.lse if lse is None else lse
+        hist = self.hist if self.shape[5] else None
+        if self.rows > 1:
+            hga.hga_attn_fwd_packed(self.p, self.q, hist, self.cap, self.k, self.v, self.idx, out, lse, stream)
+        else:
+            hga.hga_attn_decode_packed(self.p, self.q, hist, self.cap, self.k, self.v, self.n_seg, self.idx, out, lse,
+                                       stream)
+        return out, lse
+
+    def check(self, blocks=None):
+        B, Hq, Hkv, D, topk, nc = self.shape
+        G, R = Hq // Hkv, 64 if self.rows > 1 else 1
+        q, k, v, out, lse = (f64(t) for t in (self.q, self.k, self.v, self.out, self.lse))
+        for b, g, blk in np.ndindex(B, Hkv, self.blocks):
+            sl = (b, slice(g * G, (g + 1) * G), slice(blk * R, (blk + 1) * R))
+            if blocks is not None and blk not in blocks:
+                assert np.all(out[sl] == 7.0) and np.all(lse[sl] == 7.0)
+                continue
+            sel = [j for j in self.idx_host[b, g, blk] if 0 <= j < nc]
+            pick = [slice(64 * j, 64 * j + 64) for j in sel]
+            n = (blk + 1) * 64 if R > 1 else self.n_seg
+            kk = np.concatenate([self.kh[b, g, s] for s in pick] + [k[b, g, :n]])
+            vv = np.concatenate([self.vh[b, g, s] for s in pick] + [v[b, g, :n]])
+            mask = np.ones((R, len(kk)), dtype=bool)
+            if R > 1:
+                mask[:, -64:] = np.tril(np.ones((64, 64), dtype=bool))
+            o, l, mag, size = ref.attend(q[sl].reshape(G * R, D), kk, vv, np.tile(mask, (G, 1)))
+            tol, ltol = ref.attend_tol(o, mag, size, D, len(kk))
+            err = abs(out[sl].reshape(G * R, D) - o)
+            assert np.all(err <= tol), f"out {b, g, blk}: {err.max():.3e}, {np.max(err / tol):.2f} of its bound"
+            err = abs(lse[sl].reshape(-1) - l)
+            assert np.all(err <= ltol + 2.0 ** -22 * abs(l)), f"lse {b, g, blk}: {err.max():.3e}"
+
+
+# (B, Hq, Hkv, D, topk, nc, window, routes)
+DECODE = [
+    (1, 1, 1, 64, 1, 0, 1, "random"),
+    (1, 1, 1, 128, 1, 1, 1, "random"),
+    (1, 32, 8, 128, 16, 24, 37, "random"),
+    (2, 8, 2, 128, 8, 5, 16, "random"),      # routes padded with -1
+    (3, 5, 1, 64, 7, 9, 17, "holes"),
+    (2, 16, 2, 64, 40, 60, 130, "holes"),
+    (1, 7, 1, 128, 64, 70, 64, "random"),
+    (1, 6, 3, 128, 5, 9, 15, "none"),
+    (2, 4, 4, 64, 6, 9, 33, "twice"),        # a chunk named twice counts twice, as in hga_attn_decode
+    (40, 16, 8, 128, 3, 4, 300, "random"),   # more (batch, KV head) pairs than SMs
+    (5, 12, 3, 128, 21, 33, 1, "holes"),
+    (1, 8, 1, 128, 64, 64, 2000, "random"),
+]
+
+
+@pytest.mark.parametrize("case", DECODE, ids=str)
+def test_decode(case):
+    c = Packed(*case[:7], 1, routes=case[7])
+    c.run()
+    c.check()
+
+
+# (B, Hq, Hkv, topk, nc, blocks, routes)
+FWD = [
+    (1, 1, 1, 1, 0, 2, "random"),
+    (1, 4, 1, 1, 1, 2, "random"),
+    (1, 32, 8, 16, 24, 3, "random"),
+    (2, 8, 2, 8, 5, 2, "random"),
+    (1, 6, 2, 5, 9, 4, "holes"),     # three heads per KV head: one per CTA
+    (1, 4, 2, 3, 9, 5, "holes"),     # two
+    (2, 8, 1, 7, 12, 2, "random"),   # eight: two CTAs of four
+    (1, 4, 1, 64, 70, 2, "random"),
+    (1, 8, 2, 6, 9, 3, "none"),
+    (1, 4, 1, 6, 9, 2, "twice"),
+]
+
+
+@pytest.mark.parametrize("case", FWD, ids=str)
+def test_forward(case):
+    B, Hq, Hkv, topk, nc, blocks, routes = case
+    c = Packed(B, Hq, Hkv, 128, topk, nc, 64 * blocks, blocks, routes=routes)
+    c.run()
+    c.check()
+
+
+def test_forward_of_a_block_range():
+    c = Packed(1, 8, 2, 128, 4, 9, 320, 5)
+    c.p.qblock_begin, c.p.qblock_end = 1, 3
+    c.run()
+    c.check(blocks=(1, 2))
+
+
+def test_large_scores():
+    """Scores of some hundreds in either direction: the running maximum has to move."""
+    for rows in (1, 3):
+        c = Packed(1, 8, 2, 128, 12, 20, 64 * rows if rows > 1 else 70, rows, seed=4)
+        c.q *= 40
+        c.run()
+        c.check()
+
+
+@pytest.mark.parametrize("blocks", [1, 2])
+def test_non_finite_chunks_reach_only_their_rows(blocks):
+    """A chunk that holds a NaN key makes the rows that route to it NaN, and no others."""
+    import hierarchical_sparse_long_b200 as hga
+    c = Packed(1, 8, 2, 128, 3, 9, 128 if blocks == 2 else 20, blocks, seed=2)
+    bad = int(c.idx_host[0, 0, 0, 0])
+    k = torch.full((1, 1, 64, 128), 1.0, device="cuda", dtype=BF16)
+    k[0, 0, 5, 7] = float("nan")
+    one = torch.zeros(1, 1, 1, 72 * 128, device="cuda", dtype=torch.uint8)
+    hga.hga_pack_history(k, k, 64, 1, 1, 128, 0, 1, one, 1)
+    c.hist[0, 0, bad] = one[0, 0, 0]
+    out, _ = c.run()
+    for g, blk in np.ndindex(2, blocks):
+        rows = out[0, 4 * g:4 * g + 4, blk * 64:(blk + 1) * 64] if blocks > 1 else out[0, 4 * g:4 * g + 4]
+        hit = g == 0 and bad in c.idx_host[0, g, blk]
+        assert torch.all(torch.isnan(rows)) if hit else torch.all(torch.isfinite(rows))
+
+
+def test_bad_routes_are_skipped_and_flagged():
+    import hierarchical_sparse_long_b200 as hga
+    for rows, n in ((1, 30), (2, 128)):
+        c = Packed(1, 8, 2, 128, 6, 9, n, rows, seed=1)
+        c.run()
+        c.check()
+        assert hga.hga_get_device_status() == 0
+        c.idx_host[0, 1, 0, 2], c.idx_host[0, 0, 0, 4] = 9, -5
+        c.idx.copy_(torch.from_numpy(c.idx_host))
+        c.run()
+        c.check()
+        assert hga.hga_get_device_status() == hga.HGA_DEV_BAD_INDEX
+
+
+def test_offsets_beyond_32_bits():
+    """The last of 250,000 chunks of the second KV head lies 4.6 GB into the history."""
+    import hierarchical_sparse_long_b200 as hga
+    rng = np.random.default_rng(11)
+    cap, n = 250000, 6
+    hist = torch.empty(1, 2, cap, 72 * 128, device="cuda", dtype=torch.uint8)
+    kh, vh = host(keys(rng, 1, 2, n * 64, 128)), host(rng.standard_normal((1, 2, n * 64, 128)))
+    for rows, win in ((1, 10), (2, 128)):
+        c = Packed(1, 8, 2, 128, n, n, win, rows)
+        hga.hga_pack_history(kh, vh, n * 64, 1, 2, 128, cap - n, n, hist, cap)
+        _, c.kh, c.vh = ref.pack(f64(kh), f64(vh))
+        small = c.idx_host.copy()
+        c.hist, c.cap, c.p.n_hist_chunks = hist, cap, cap
+        c.idx = torch.from_numpy(np.where(small >= 0, small + cap - n, -1)).cuda().to(torch.int32)
+        c.run()
+        c.check()
+    k2, v2 = torch.empty_like(kh), torch.empty_like(vh)
+    hga.hga_unpack_history(hist, cap, 1, 2, 128, cap - n, n, k2, v2, n * 64)
+    assert np.array_equal(f64(k2), c.kh) and np.array_equal(f64(v2), c.vh)
+
+
+def test_repeated_graph_and_two_streams():
+    """Equal inputs give equal bits: again, replayed from a graph on another stream, and with a
+    second call under way."""
+    for rows, n, batch in ((1, 100, 3), (4, 256, 1)):
+        c, other = Packed(batch, 16, 4, 128, 9, 20, n, rows), Packed(batch, 8, 2, 128, 7, 20, n, rows, seed=3)
+        out, lse = (t.clone() for t in c.run())
+        other.run()
+        other.check()
+        want = other.out.clone()
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            c.run()
+        side = torch.cuda.Stream()
+        for _ in range(3):
+            c.out.fill_(7.0)
+            other.out.fill_(7.0)
+            torch.cuda.synchronize()
+            with torch.cuda.stream(side):
+                other.run()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(c.out, out) and torch.equal(c.lse, lse) and torch.equal(other.out, want)
+        del graph
+
+
+# ------------------------------------------------------------------ together
+def test_projection_to_packed_attention():
+    """The operators as a layer uses them: projections normed, rotated and laid out; closed
+    chunks detached into the packed history with their summaries; the next segment and then
+    single tokens routed over those and attended; the segment's gradients taken back to the
+    projections.  Every step is compared with its formula on that step's own inputs."""
+    import hierarchical_sparse_long_b200 as hga
+    B, Hq, Hkv, D, S, topk = 1, 8, 2, 128, 256, 3
+    rng = np.random.default_rng(21)
+    row = (Hq + 2 * Hkv) * D
+    table = torch.empty(1024, D, device="cuda")
+    hga.hga_rope_table(1e6, D, 1024, table)
+    wq, wk = host(1 + 0.1 * rng.standard_normal(D)), host(1 + 0.1 * rng.standard_normal(D))
+
+    def project(first, n, k, v):
+        x = host(rng.standard_normal((B, n, row)))
+        q = torch.empty(B, Hq, n, D, device="cuda", dtype=BF16)
+        p = hga.ProjParams(B, Hq, Hkv, D, n, D, kv_head_stride=S, first_pos=first)
+        hga.hga_qk_norm_rope(p, x, x[..., Hq * D:], x[..., (Hq + Hkv) * D:], wq, wk, table, None, q, k, v)
+        cs = ref.rope_table(1e6, D, 1024)[first:first + n].astype(np.float64)[None, None]
+        heads = f64(x).reshape(B, n, -1, D).swapaxes(1, 2)
+        y, mag = ref.norm_rope(heads[:, :Hq], f64(wq), cs, D, 1e-6)
+        assert np.all(abs(f64(q) - y) <= ref.HALF["bf16"] * abs(y) + 32 * ref.U32 * mag)
+        return p, x, q
+
+    kw = torch.empty(B, Hkv, S, D, device="cuda", dtype=BF16)
+    vw = torch.empty_like(kw)
+    nc = S // 64
+    cap = 3 * nc
+    hist = torch.zeros(B, Hkv, cap, hga.hga_packed_chunk_bytes(D), device="cuda", dtype=torch.uint8)
+    summ = torch.zeros(B, Hkv, cap, D, device="cuda")
+    project(0, S, kw, vw)
+    hga.hga_pack_history(kw, vw, S, B, Hkv, D, 0, nc, hist, cap, summ, cap)
+    _, kh, vh = ref.pack(f64(kw), f64(vw))
+
+    # the next segment
+    p, x, q = project(S, S, kw, vw)
+    c = Packed(B, Hq, Hkv, D, topk, nc, S, nc, stride_extra=0)
+    c.hist, c.cap, c.kh, c.vh, c.q, c.k, c.v = hist, cap, kh, vh, q, kw, vw
+    hga.hga_route(c.p, q, summ, cap, c.idx)
+    c.idx_host = c.idx.cpu().numpy()
+    assert np.all(c.idx_host >= 0)
+    out, lse = c.run()
+    c.check()
+
+    # its gradients: the backward over the unpacked values of the same chunks
+    k2, v2 = torch.empty(B, Hkv, nc * 64, D, device="cuda", dtype=BF16), torch.empty_like(kw)
+    hga.hga_unpack_history(hist, cap, B, Hkv, D, 0, nc, k2, v2, nc * 64)
+    out2, lse2 = torch.empty_like(out), torch.empty_like(lse)
+    hga.hga_attn_fwd(c.p, q, k2, v2, kw, vw, c.idx, out2, lse2)
+    hc.compare(hc.f32(out), hc.f32(out2), "bf16", "forward over the unpacked values")
+    dout = host(rng.standard_normal((B, Hq, S, D)))
+    dq = torch.empty(B, Hq, S, D, device="cuda")
+    dk, dv = torch.empty(B, Hkv, S, D, device="cuda"), torch.empty(B, Hkv, S, D, device="cuda")
+    ws = torch.empty(hga.hga_attn_bwd_workspace_size(c.p) // 4 + 1, device="cuda")
+    hga.hga_attn_bwd(c.p, q, k2, v2, kw, vw, c.idx, out, lse, dout, dq, dk, dv, ws)
+    dx = torch.empty_like(x)
+    dwq, dwk = torch.empty(D, device="cuda"), torch.empty(D, device="cuda")
+    wsp = torch.empty(hga.hga_qk_norm_rope_workspace_size(p), device="cuda", dtype=torch.uint8)
+    hga.hga_qk_norm_rope_bwd(p, x, x[..., Hq * D:], wq, wk, table, None, dq, dk, dv, dx, dx[..., Hq * D:],
+                             dx[..., (Hq + Hkv) * D:], dwq, dwk, wsp)
+    want = _layer_grad(x, wq, wk, table[S:2 * S], c, dout)
+    for got, w, what in ((dx, want[0], "dx"), (dwq, want[1], "dwq"), (dwk, want[2], "dwk")):
+        # bf16 q, k, P, dS and dx on the way: a relative error of a few 2^-8 in norm, 8 allowed
+        err = np.linalg.norm(f64(got) - w) / np.linalg.norm(w)
+        assert err < 8 * ref.HALF["bf16"], f"{what}: {err:.2e}"
+
+    # the segment closes; a token at a time follows
+    hga.hga_pack_history(kw, vw, S, B, Hkv, D, nc, nc, hist, cap, summ, cap)
+    _, ks, vs = ref.pack(f64(kw), f64(vw))
+    kh, vh = np.concatenate([kh, ks], axis=2), np.concatenate([vh, vs], axis=2)
+    for t in range(2):
+        _, _, q = project(2 * S + t, 1, kw[:, :, t:], vw[:, :, t:])
+        c = Packed(B, Hq, Hkv, D, topk, 2 * nc, t + 1, 1, stride_extra=S - t - 1)
+        c.rows = 1
+        c.hist, c.cap, c.kh, c.vh, c.q, c.k, c.v = hist, cap, kh, vh, q, kw, vw
+        hga.hga_route(c.p, q, summ, cap, c.idx)
+        c.idx_host = c.idx.cpu().numpy()
+        c.run()
+        c.check()
+
+
+def _layer_grad(x, wq, wk, cs, c, dout):
+    """Gradients of sum(dout * out) of the segment by torch's differentiation in 64 bits."""
+    B, Hq, Hkv, D, topk, nc = c.shape
+    x, wq, wk = (t.detach().double().requires_grad_() for t in (x, wq, wk))
+    S, G, h = x.shape[1], Hq // Hkv, D // 2
+    cos, sin = cs.double()[:, :h], cs.double()[:, h:]
+
+    def rot(y, w):
+        n = y * (y.square().mean(-1, keepdim=True) + 1e-6).rsqrt() * w
+        return torch.cat([n[..., :h] * cos - n[..., h:] * sin, n[..., h:] * cos + n[..., :h] * sin], dim=-1)
+
+    heads = x.view(B, S, Hq + 2 * Hkv, D).transpose(1, 2)
+    q, k, v = rot(heads[:, :Hq], wq), rot(heads[:, Hq:Hq + Hkv], wk), heads[:, Hq + Hkv:]
+    kh, vh = torch.from_numpy(c.kh).cuda(), torch.from_numpy(c.vh).cuda()
+    loss = 0.0
+    for g, blk in np.ndindex(Hkv, S // 64):
+        sel = torch.cat([torch.arange(64) + 64 * int(j) for j in c.idx_host[0, g, blk]]).cuda()
+        n = 64 * (blk + 1)
+        kk, vv = torch.cat([kh[0, g][sel], k[0, g, :n]]), torch.cat([vh[0, g][sel], v[0, g, :n]])
+        r = slice(64 * blk, n)
+        s = q[0, g * G:(g + 1) * G, r] @ kk.T * D ** -0.5
+        s[..., -64:] += torch.full((64, 64), -torch.inf, device="cuda", dtype=torch.float64).triu(1)
+        loss = loss + (dout[0, g * G:(g + 1) * G, r].double() * (s.softmax(-1) @ vv)).sum()
+    loss.backward()
+    return f64(x.grad), f64(wq.grad), f64(wk.grad)
