@@ -262,17 +262,27 @@ __global__ void __launch_bounds__(32 * (kIssueWarps + 4 * NH + kProdWarps), 1)
                                                                    a.status)))
                         break;
                     tc::fence_after_sync();
-                    const bool hist = t < n_hist;
-                    const uint64_t vd = (hist ? v_hist : v_seg) + (uint64_t)((s * KV_TILE_BYTES) >> 4);
-                    const uint32_t vstep = hist ? 32 >> 4 : 2048 >> 4;  // 16 tokens on
-                    const uint32_t idesc = hist ? IDESC_PV_HIST : IDESC_PV;
-                    // P(t) as bf16 pairs in the first 32 columns of S buffer pb: 8 columns per K step
+                    // P(t) as bf16 pairs in the first 32 columns of S buffer pb: 8 columns per K step.
+                    // The instruction descriptors are constants: with a run-time one an issue
+                    // takes twice as long.
                     const uint32_t pa = tmem + 256 + 128 * h + 64 * pb;
+                    const uint64_t voff = (uint64_t)((s * KV_TILE_BYTES) >> 4);
+                    if (t < n_hist) {
 #pragma unroll
-                    for (int kk = 0; kk < TILE / 16; ++kk) {
-                        if (tc::elect_one())
-                            mma_f16_ts(o_tmem, pa + 8 * kk, vd + kk * vstep, idesc, (t > 0 || kk > 0) ? 1u : 0u);
-                        __syncwarp();
+                        for (int kk = 0; kk < TILE / 16; ++kk) {
+                            if (tc::elect_one())
+                                mma_f16_ts(o_tmem, pa + 8 * kk, v_hist + voff + (uint64_t)(kk * (32 >> 4)),
+                                           IDESC_PV_HIST, (t > 0 || kk > 0) ? 1u : 0u);
+                            __syncwarp();
+                        }
+                    } else {
+#pragma unroll
+                        for (int kk = 0; kk < TILE / 16; ++kk) {
+                            if (tc::elect_one())
+                                mma_f16_ts(o_tmem, pa + 8 * kk, v_seg + voff + (uint64_t)(kk * (2048 >> 4)), IDESC_PV,
+                                           (t > 0 || kk > 0) ? 1u : 0u);
+                            __syncwarp();
+                        }
                     }
                     if (tc::elect_one()) {
                         tc::mma_commit(&bars->o_done[h][pb]);
@@ -317,26 +327,23 @@ __global__ void __launch_bounds__(32 * (kIssueWarps + 4 * NH + kProdWarps), 1)
             }
             __syncwarp();
         };
-        // widened codes are visible to the tensor core before the warp arrives
-        auto publish = [&](uint64_t *bar) {
-            tc::fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(bar);
-        };
+        // A thread holds the codes and grids of one tile ahead.  They are asked for behind
+        // the tile's only proxy fence: a fence waits for the loads in flight before it, so
+        // one between K and V would wait for memory twice a tile.
         KShare ks;
         VShare vs;
-        if (n_hist > 0) {
-            const uint8_t *rec = base + (long long)bars->tiles[0] * Packed<D>::kRecord;
+        auto load = [&](int j) {
+            const uint8_t *rec = base + (long long)bars->tiles[j] * Packed<D>::kRecord;
             ks.load(rec, ko, kr);
             vs.load(rec + Packed<D>::kPart, vo, vr);
-        }
+        };
+        if (n_hist > 0) load(0);
         for (int j = 0; j < n_tiles; ++j) {
             const int s = j % NSTAGE, u = j / NSTAGE;
-            const uint8_t *next =
-                j + 1 < n_hist ? base + (long long)bars->tiles[j + 1] * Packed<D>::kRecord : nullptr;
             // a stage frees once the products of the tile NSTAGE back have read it
             if (j >= NSTAGE &&
-                !__all_sync(0xffffffffu, tc::mbar_wait(&bars->k_empty[s], (u - 1) & 1, abort, a.status)))
+                !__all_sync(0xffffffffu, tc::mbar_wait(&bars->k_empty[s], (u - 1) & 1, abort, a.status) &&
+                                             tc::mbar_wait(&bars->v_empty[s], (u - 1) & 1, abort, a.status)))
                 break;
             if (j < n_hist) {
 #pragma unroll
@@ -345,28 +352,25 @@ __global__ void __launch_bounds__(32 * (kIssueWarps + 4 * NH + kProdWarps), 1)
                     packed_octet(ks.w[i], ks.s, ks.z, r);
                     tc::st_shared_v4(kdst + s * KV_TILE_BYTES + i * 8 * 128, r[0], r[1], r[2], r[3]);
                 }
-                publish(&bars->k_full[s]);
-                if (next) ks.load(next, ko, kr);
-            } else {
-                seg_tile(smem + L::K + s * KV_TILE_BYTES, &tm_ks, j, &bars->k_full[s]);
-            }
-            issued = 2 * j + 1;
-            if (j >= NSTAGE &&
-                !__all_sync(0xffffffffu, tc::mbar_wait(&bars->v_empty[s], (u - 1) & 1, abort, a.status)))
-                break;
-            if (j < n_hist) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     uint32_t r[4];
                     packed_octet(vs.w[i], vs.s[i >> 2], vs.z[i >> 2], r);
                     tc::st_shared_v4(vdst + s * KV_TILE_BYTES + i * 16 * 128, r[0], r[1], r[2], r[3]);
                 }
-                publish(&bars->v_full[s]);
-                if (next) vs.load(next + Packed<D>::kPart, vo, vr);
+                // widened codes are visible to the tensor core before the warp arrives
+                tc::fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) {
+                    tc::mbar_arrive(&bars->k_full[s]);
+                    tc::mbar_arrive(&bars->v_full[s]);
+                }
+                if (j + 1 < n_hist) load(j + 1);
             } else {
+                seg_tile(smem + L::K + s * KV_TILE_BYTES, &tm_ks, j, &bars->k_full[s]);
                 seg_tile(smem + L::V + s * KV_TILE_BYTES, &tm_vs, j, &bars->v_full[s]);
             }
-            issued = 2 * j + 2;
+            issued = j + 1;
         }
     } else {
         // -------------------------------------------------------------- softmax / epilogue
@@ -500,14 +504,13 @@ __global__ void __launch_bounds__(32 * (kIssueWarps + 4 * NH + kProdWarps), 1)
         // shared memory and TMEM are released
         int never = 0;
         if (warp == kProd0 && lane == 0) {
-            // stages whose segment tiles this thread loaded last (K tiles 0 .. nk - 1, V
-            // tiles 0 .. nv - 1); their barriers complete once the other producer warps
-            // have arrived too, which an aborting one may not have: the wait is bounded
-            const int nk = (issued + 1) / 2, nv = issued / 2;
-            for (int j = nk - NSTAGE < n_hist ? n_hist : nk - NSTAGE; j < nk; ++j)
+            // stages whose segment tiles this thread sent for last; their barriers complete
+            // once the other producer warps have arrived too, which an aborting one may not
+            // have: the wait is bounded
+            for (int j = issued - NSTAGE < n_hist ? n_hist : issued - NSTAGE; j < issued; ++j) {
                 tc::mbar_wait(&bars->k_full[j % NSTAGE], (j / NSTAGE) & 1, &never, a.status, 1ll << 28);
-            for (int j = nv - NSTAGE < n_hist ? n_hist : nv - NSTAGE; j < nv; ++j)
                 tc::mbar_wait(&bars->v_full[j % NSTAGE], (j / NSTAGE) & 1, &never, a.status, 1ll << 28);
+            }
             tc::mbar_wait(&bars->q_full, 0, &never, a.status, 1ll << 28);
         }
         if (warp < kIssueWarps && (warp >> 1) < NH) {
