@@ -116,6 +116,22 @@ __device__ __forceinline__ bool wait_count(int *counter, int target, volatile in
     return true;
 }
 
+// (x0, x1) y + z, and (d0, d1) += (x0, x1): two elements per instruction.
+__device__ __forceinline__ void fma2(float &x0, float &x1, float y, float z) {
+    asm("{\n\t.reg .b64 a, b, c;\n\t"
+        "mov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\tmov.b64 c, {%3, %3};\n\t"
+        "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "+f"(x0), "+f"(x1)
+        : "f"(y), "f"(z));
+}
+__device__ __forceinline__ void add2(float &d0, float &d1, float x0, float x1) {
+    asm("{\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+        "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "+f"(d0), "+f"(d1)
+        : "f"(x0), "f"(x1));
+}
+
 // Codes and grid of one thread's share of a K part: octet `o` of the tokens r0 + 8 i.
 struct KShare {
     uint32_t w[8], s[4], z[4];
@@ -409,13 +425,16 @@ __global__ void __launch_bounds__(32 * (kIssueWarps + 4 * NH + kProdWarps), 1)
                 for (int c = 0; c < 64; ++c)
                     if (c > i) x[c] = -INFINITY;
             }
-            // row max of the raw scores (the scale is positive), 8 independent chains
-            float mpart[8];
+            // row max of the raw scores (the scale is positive), 4 chains of three-way maxima
+            float mpart[4];
 #pragma unroll
-            for (int c = 0; c < 64; ++c) mpart[c & 7] = (c < 8) ? x[c] : fmaxf(mpart[c & 7], x[c]);
-            const float mx = fmaxf(fmaxf(fmaxf(mpart[0], mpart[1]), fmaxf(mpart[2], mpart[3])),
-                                   fmaxf(fmaxf(mpart[4], mpart[5]), fmaxf(mpart[6], mpart[7]))) *
-                             a.scale_log2;
+            for (int c = 0; c < 4; ++c) {
+                mpart[c] = x[c];
+#pragma unroll
+                for (int e = c + 4; e < TILE; e += 8)
+                    mpart[c] = e + 4 < TILE ? fmaxf(fmaxf(mpart[c], x[e]), x[e + 4]) : fmaxf(mpart[c], x[e]);
+            }
+            const float mx = fmaxf(fmaxf(mpart[0], mpart[1]), fmaxf(mpart[2], mpart[3])) * a.scale_log2;
             // Lazy rescaling: the reference max only moves when the row max grows by
             // more than kRescaleLog2, so P stays <= 2^kRescaleLog2 and O is rescaled
             // in TMEM only on those (rare) tiles.
@@ -424,15 +443,23 @@ __global__ void __launch_bounds__(32 * (kIssueWarps + 4 * NH + kProdWarps), 1)
             const float alpha = grow ? tc::ex2(m_run - m_use) : 1.f;
             // a row with no unmasked key yet keeps m = -inf; its p must come out 0, not NaN
             const float m_sub = m_use == -INFINITY ? 0.f : m_use;
-            float spart[8];
+            // p = 2^(s * log2(e)/sqrt(D) - m), two elements per FMA and sum instruction
+            float sp[4][2];
 #pragma unroll
-            for (int c = 0; c < 64; ++c) {
-                // p = 2^(s * log2(e)/sqrt(D) - m)
-                x[c] = tc::ex2(fmaf(x[c], a.scale_log2, -m_sub));
-                spart[c & 7] = (c < 8) ? x[c] : spart[c & 7] + x[c];
+            for (int c = 0; c < TILE; c += 2) {
+                fma2(x[c], x[c + 1], a.scale_log2, -m_sub);
+                x[c] = tc::ex2(x[c]);
+                x[c + 1] = tc::ex2(x[c + 1]);
+                float (&q)[2] = sp[(c >> 1) & 3];
+                if (c < 8) {
+                    q[0] = x[c];
+                    q[1] = x[c + 1];
+                } else {
+                    add2(q[0], q[1], x[c], x[c + 1]);
+                }
             }
-            const float sum = ((spart[0] + spart[1]) + (spart[2] + spart[3])) +
-                              ((spart[4] + spart[5]) + (spart[6] + spart[7]));
+            const float sum = ((sp[0][0] + sp[1][0]) + (sp[2][0] + sp[3][0])) +
+                              ((sp[0][1] + sp[1][1]) + (sp[2][1] + sp[3][1]));
             l_run = l_run * alpha + sum;
             const int pb = j & 1;
             // a rescale needs O complete up to tile j-1 (PV(j-1) done) before PV(j) adds to it;
