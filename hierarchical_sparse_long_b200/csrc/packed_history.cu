@@ -7,15 +7,18 @@
 // Grid of a group with extremes mn, mx (K: a channel's 64 tokens, V: 64 channels of a
 // token), c nearest to the value, ties to even:
 //   s = bf16(fl(fl(mx - mn) / 15)), 0 below 2^-100
-//   z = bf16(fl(mn - 16 s)),   c = clamp(rne((x - z) / s) - 16, 0, 15), 0 where s = 0
+//   z = bf16(fl(mn - 16 s)),   c = clamp(rne(fl(x - z) / s) - 16, 0, 15), 0 where s = 0
 // s and z are rounded first and the codes chosen for the rounded grid, so their
-// rounding moves the grid and not the choice.  s = z = NaN when the group's sum is not
-// finite (a NaN or an infinity in it) or s or z is not: its values read as NaN.
+// rounding moves the grid and not the choice.  s = z = NaN when an element is not finite
+// (the extremes propagate NaN, an infinity makes s infinite) or s or z is not: the
+// group's values read as NaN.
 //
 // pack is bound by HBM: K and V are read once (the summaries come from the same read),
-// and 0.28 of their bytes written.  One 256-thread CTA takes a chunk, all 32 KiB of its
-// loads in flight; K's extremes and sums cross threads through shared memory, V's stay
-// in the lanes of a row, and V's codes are turned there from token to channel order.
+// and 0.28 of their bytes written.  One 256-thread CTA takes a chunk, all of its loads in
+// flight; K's extremes and sums cross threads through shared memory, V's stay in the lanes
+// of a row, and V's codes are turned there from token to channel order.  Choosing 16,384
+// codes a chunk costs about as much issue time as its bytes cost bandwidth, so the choice
+// is made of two-element FMAs and one multiply-add into the word.
 #include <cfloat>
 
 #include "packed.cuh"
@@ -33,39 +36,166 @@ struct Grid {
 
 __device__ __forceinline__ float bf16_round(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
 
-__device__ __forceinline__ Grid make_grid(float mn, float mx, float sum) {
+__device__ __forceinline__ Grid make_grid(float mn, float mx) {
     Grid g;
     g.s = bf16_round(__fdiv_rn(mx - mn, 15.f));
     if (g.s < 0x1p-100f) g.s = 0.f;
     g.z = bf16_round(fmaf(-16.f, g.s, mn));
     // fabsf(NaN) <= FLT_MAX is false
-    if (!(fabsf(sum) <= FLT_MAX) || !(fabsf(g.s) <= FLT_MAX) || !(fabsf(g.z) <= FLT_MAX))
-        g.s = g.z = __int_as_float(0x7FC00000);
+    if (!(fabsf(g.s) <= FLT_MAX) || !(fabsf(g.z) <= FLT_MAX)) g.s = g.z = __int_as_float(0x7FC00000);
     return g;
 }
 
-// The code of x on grid g; inv = 1 / s.  t * inv is within 2^-22 of the quotient
-// relatively (below 2^-17 in all), so unless it lies that close to a border its
-// nearest integer is the quotient's; those that do are decided in 64 bits.
-__device__ __forceinline__ uint32_t code_of(float x, const Grid &g, float inv) {
-    const float q = (x - g.z) * inv;
-    float k = rintf(q);
-    if (fabsf(fabsf(q - k) - 0.5f) < 0x1p-15f) k = (float)rint(((double)x - (double)g.z) / (double)g.s);
-    // a NaN grid compares false both ways and becomes code 0
-    return k > 16.f ? (uint32_t)(fminf(k, 31.f) - 16.f) : 0u;
+// s in the low and z in the high half of a word.
+__device__ __forceinline__ uint32_t grid_bits(const Grid &g) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(g.s, g.z);
+    return *reinterpret_cast<const uint32_t *>(&b);
+}
+__device__ __forceinline__ Grid grid_of(uint32_t b) {
+    return {__uint_as_float(b << 16), __uint_as_float(b & 0xFFFF0000u)};
 }
 
-__device__ __forceinline__ float grid_inv(const Grid &g) { return g.s > 0.f ? 1.f / g.s : 0.f; }
+// 1 / (15 s) to within 2^-21, 0 for s = 0 (every element is code 0).
+__device__ __forceinline__ float grid_inv(float s) { return s == 0.f ? 0.f : __fdividef(1.f / 15.f, s); }
 
-__device__ __forceinline__ uint16_t bf16_bits(float x) {
-    const __nv_bfloat16 b = __float2bfloat16_rn(x);
-    return *reinterpret_cast<const uint16_t *>(&b);
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// Where the nibble of a word's element e starts, and of a staged byte.
+template <bool kNibble> __device__ constexpr int code_shift(int e) {
+    return kNibble ? 4 * (e >> 1) + 16 * (e & 1) : 8 * e;
+}
+
+// Codes of N elements in a word, approximated: p = (x - z) / (15 s) - 16/15 saturates to
+// [0, 1] and 15 p is within 2^-17 of the quotient.  Rounding it to 2^-14 turns what lies that
+// close to a border into a tie, which the rounding to an integer (adding 1.5 2^23 leaves the
+// integer in the low bits) gives to the even code.  A true tie belongs there; an element
+// that does not is more than half a step from its code, and r = x - z - (16 + c) s tells,
+// exactly: r[e] is for the caller to compare with s / 2.
+template <int N, bool kNibble>
+__device__ __forceinline__ uint32_t codes(const float (&x)[N], const float (&ss)[N], const float (&zs)[N],
+                                          const float (&inv)[N], float (&r)[N]) {
+    constexpr float magic = 12582912.f, magic14 = 768.f;  // ulp 1 and 2^-14
+    constexpr uint32_t magic_bits = 0x4B400000u;
+    uint32_t w = 0, off = 0;
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+        const float2 y = __fadd2_rn(make_float2(x[e], x[e + 1]), make_float2(-zs[e], -zs[e + 1]));
+        const float2 p = make_float2(__saturatef(fmaf(y.x, inv[e], -16.f / 15.f)),
+                                     __saturatef(fmaf(y.y, inv[e + 1], -16.f / 15.f)));
+        const float2 u = __fadd2_rn(__ffma2_rn(p, make_float2(15.f, 15.f), make_float2(magic14, magic14)),
+                                    make_float2(-magic14, -magic14));
+        const float2 t = __fadd2_rn(u, make_float2(magic, magic));
+        const float2 k = __fadd2_rn(t, make_float2(16.f - magic, 16.f - magic));
+        const float2 d = __ffma2_rn(k, make_float2(-ss[e], -ss[e + 1]), y);
+        r[e] = d.x;
+        r[e + 1] = d.y;
+        // the constant bits of t add up to a constant, modulo 2^32
+        w += __float_as_uint(t.x) * (1u << code_shift<kNibble>(e));
+        w += __float_as_uint(t.y) * (1u << code_shift<kNibble>(e + 1));
+        off += (magic_bits << code_shift<kNibble>(e)) + (magic_bits << code_shift<kNibble>(e + 1));
+    }
+    return w - off;
+}
+
+// A code, at most one off, decided by the exact borders (16 + k +- 1/2) s (6 bits x 8 bits).
+__device__ __forceinline__ uint32_t exact_code(float x, const Grid &g, uint32_t k) {
+    const float y = __fsub_rn(x, g.z);
+    const float up = (16.5f + (float)k) * g.s, dn = (15.5f + (float)k) * g.s;
+    const bool odd = k & 1;
+    if (y > up || (y == up && odd))
+        k = k < 15u ? k + 1u : k;
+    else if (y < dn || (y == dn && odd))
+        k = k > 0u ? k - 1u : k;
+    // a NaN grid fails every comparison and keeps code 0; s = 0 has only code 0
+    return g.s == 0.f ? 0u : k;
+}
+
+// A word's codes decided again: four elements of one grid staged as bytes, or the 16 bytes
+// of elements (8 or 4) with a grid each as nibbles.  Few warps come here: one element in 2^15
+// of arbitrary ones, and groups whose z lost more than half a step to its rounding; calls,
+// so that the common path holds neither their code nor their registers.
+__device__ __noinline__ uint32_t exact_bytes(float x0, float x1, float x2, float x3, uint32_t grid, uint32_t word) {
+    const Grid g = grid_of(grid);
+    return exact_code(x0, g, word & 15u) | exact_code(x1, g, word >> 8 & 15u) << 8 |
+           exact_code(x2, g, word >> 16 & 15u) << 16 | exact_code(x3, g, word >> 24 & 15u) << 24;
+}
+template <typename T>
+__device__ __noinline__ uint32_t exact_nibbles(uint4 x, const uint32_t *grids, uint32_t word) {
+    constexpr int N = Vec16<T>::N;
+    const uint32_t raw[4] = {x.x, x.y, x.z, x.w};
+    uint32_t w = 0;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        const int sh = code_shift<true>(e);
+        const float f = __uint_as_float(N == 4 ? raw[e % 4] : (e & 1 ? raw[e / 2 % 4] & 0xFFFF0000u : raw[e / 2 % 4] << 16));
+        w |= exact_code(f, grid_of(grids[e]), word >> sh & 15u) << sh;
+    }
+    return w;
+}
+
+// Extremes of elements, NaN if one is NaN.  For bf16 the word (-min, max) of a pair of
+// halves, so that one instruction keeps both; for fp32 two floats.
+template <typename T> struct Ext;
+template <> struct Ext<__nv_bfloat16> {
+    uint32_t w;
+    __device__ __forceinline__ static uint32_t max2(uint32_t a, uint32_t b) {
+        uint32_t r;
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    __device__ __forceinline__ static Ext row(const uint4 &u) {  // of 8 elements
+        const uint32_t hi = max2(max2(u.x, u.y), max2(u.z, u.w));
+        const uint32_t lo = max2(max2(u.x ^ 0x80008000u, u.y ^ 0x80008000u), max2(u.z ^ 0x80008000u, u.w ^ 0x80008000u));
+        return {max2(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632))};
+    }
+    __device__ __forceinline__ Ext with(Ext o) const { return {max2(w, o.w)}; }
+    __device__ __forceinline__ Ext shfl(int o) const { return {__shfl_xor_sync(0xffffffffu, w, o)}; }
+    __device__ __forceinline__ float mn() const { return -__uint_as_float(w << 16); }
+    __device__ __forceinline__ float mx() const { return __uint_as_float(w & 0xFFFF0000u); }
+};
+template <> struct Ext<float> {
+    float lo, hi;
+    __device__ __forceinline__ static Ext row(const uint4 &u) {  // of 4 elements
+        const float x[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
+        return {min_nan(min_nan(x[0], x[1]), min_nan(x[2], x[3])), max_nan(max_nan(x[0], x[1]), max_nan(x[2], x[3]))};
+    }
+    __device__ __forceinline__ Ext with(Ext o) const { return {min_nan(lo, o.lo), max_nan(hi, o.hi)}; }
+    __device__ __forceinline__ Ext shfl(int o) const {
+        return {__shfl_xor_sync(0xffffffffu, lo, o), __shfl_xor_sync(0xffffffffu, hi, o)};
+    }
+    __device__ __forceinline__ float mn() const { return lo; }
+    __device__ __forceinline__ float mx() const { return hi; }
+};
+
+template <typename T> __device__ __forceinline__ uint32_t word_min(uint32_t a, uint32_t b) {  // lane-wise, NaN kept
+    if constexpr (sizeof(T) == 2) {
+        uint32_t r;
+        asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    } else {
+        return __float_as_uint(min_nan(__uint_as_float(a), __uint_as_float(b)));
+    }
+}
+template <typename T> __device__ __forceinline__ uint32_t word_max(uint32_t a, uint32_t b) {
+    if constexpr (sizeof(T) == 2)
+        return Ext<__nv_bfloat16>::max2(a, b);
+    else
+        return __float_as_uint(max_nan(__uint_as_float(a), __uint_as_float(b)));
 }
 
 // Thread (col, slot) owns VEC channels of the rows slot, slot + NSLOT, ...: the split of
 // summaries_kernel, whose sums are repeated here in the same order bit for bit.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) pack_kernel(const T *__restrict__ k, const T *__restrict__ v,
+__global__ void __launch_bounds__(kThreads, 3) pack_kernel(const T *__restrict__ k, const T *__restrict__ v,
                                                         long long head_stride, int n_chunks, int first_chunk,
                                                         uint8_t *__restrict__ hist, long long cap,
                                                         float *__restrict__ summ, long long summ_cap) {
@@ -75,8 +205,10 @@ __global__ void __launch_bounds__(kThreads) pack_kernel(const T *__restrict__ k,
     constexpr int NSLOT = kThreads / LPR;
     constexpr int ROWS = kChunk / NSLOT;
     constexpr int CS = D + 4;  // row stride of the staged V codes, bytes
-    __shared__ float part[3][NSLOT][D + 1];
-    __shared__ Grid kgrid[D];
+    constexpr int WPR = D * (int)sizeof(T) / 4;  // words of a row
+    __shared__ __align__(16) float part_sum[NSLOT][D + 4];
+    __shared__ __align__(16) uint32_t part_mn[NSLOT][WPR + 4], part_mx[NSLOT][WPR + 4];
+    __shared__ __align__(16) uint32_t kgrid[D];
     __shared__ __align__(16) uint8_t vcodes[kChunk * CS];
     const int tid = threadIdx.x;
     const long long slice = blockIdx.x / n_chunks;
@@ -86,96 +218,136 @@ __global__ void __launch_bounds__(kThreads) pack_kernel(const T *__restrict__ k,
     const long long row0 = slice * head_stride + (long long)j * kChunk;
     uint8_t *rec = hist + (slice * cap + first_chunk + j) * P::kRecord;
 
-    float x[ROWS][VEC], y[ROWS][VEC];
+    // the rows as they lie in memory; widened where they are used
+    uint4 xr[ROWS], yr[ROWS];
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) Vec16<T>::load(k + (row0 + slot + r * NSLOT) * D + col, x[r]);
+    for (int r = 0; r < ROWS; ++r) xr[r] = *reinterpret_cast<const uint4 *>(k + (row0 + slot + r * NSLOT) * D + col);
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) Vec16<T>::load(v + (row0 + slot + r * NSLOT) * D + col, y[r]);
+    for (int r = 0; r < ROWS; ++r) yr[r] = *reinterpret_cast<const uint4 *>(v + (row0 + slot + r * NSLOT) * D + col);
+    auto widen = [](const uint4 &u, float (&f)[VEC]) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (VEC == 8) {
+                f[2 * i] = __uint_as_float(w[i] << 16);
+                f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            } else {
+                f[i] = __uint_as_float(w[i]);
+            }
+        }
+    };
 
     // K: extremes and sum of every channel
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-        float sum = 0.f, mn = x[0][e], mx = x[0][e];
+    {
+        float sum[VEC];
+        uint4 mn = xr[0], mx = xr[0];
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
-            sum += x[r][e];
-            mn = fminf(mn, x[r][e]);
-            mx = fmaxf(mx, x[r][e]);
-        }
-        part[0][slot][col + e] = sum;
-        part[1][slot][col + e] = mn;
-        part[2][slot][col + e] = mx;
-    }
-    __syncthreads();
-    if (tid < D) {
-        float sum = 0.f, mn = part[1][0][tid], mx = part[2][0][tid];
+            float x[VEC];
+            widen(xr[r], x);
 #pragma unroll
-        for (int s = 0; s < NSLOT; ++s) {
-            sum += part[0][s][tid];
-            mn = fminf(mn, part[1][s][tid]);
-            mx = fmaxf(mx, part[2][s][tid]);
+            for (int e = 0; e < VEC; ++e) sum[e] = (r ? sum[e] : 0.f) + x[e];
+            if (r) {
+                mn = make_uint4(word_min<T>(mn.x, xr[r].x), word_min<T>(mn.y, xr[r].y), word_min<T>(mn.z, xr[r].z),
+                                word_min<T>(mn.w, xr[r].w));
+                mx = make_uint4(word_max<T>(mx.x, xr[r].x), word_max<T>(mx.y, xr[r].y), word_max<T>(mx.z, xr[r].z),
+                                word_max<T>(mx.w, xr[r].w));
+            }
         }
-        const Grid g = make_grid(mn, mx, sum);
-        kgrid[tid] = g;
-        uint16_t *gs = reinterpret_cast<uint16_t *>(rec + P::kGridOff);
-        gs[tid] = bf16_bits(g.s);
-        gs[D + tid] = bf16_bits(g.z);
-        if (summ) summ[(slice * summ_cap + first_chunk + j) * D + tid] = sum / (float)kChunk;
+#pragma unroll
+        for (int e = 0; e < VEC; e += 4)
+            *reinterpret_cast<float4 *>(&part_sum[slot][col + e]) = make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
+        *reinterpret_cast<uint4 *>(&part_mn[slot][4 * lane_col]) = mn;
+        *reinterpret_cast<uint4 *>(&part_mx[slot][4 * lane_col]) = mx;
     }
 
-    // V: the grid of every token and 64 channels, from the lanes that hold them
+    // V: the extremes of every token and 64 channels lie in GL lanes.  Each exchange halves
+    // the rows that a lane goes on with, until one is left; that lane makes the row's grid.
     constexpr int GL = 64 / VEC;  // lanes per group
-    uint16_t *vs = reinterpret_cast<uint16_t *>(rec + P::kPart + P::kGridOff);
+    constexpr int PER = GL / ROWS;  // lanes that end up with the same row
+    static_assert(PER >= 1, "a row's lanes outnumber the rows of a thread");
+    uint32_t vgrid[ROWS];
+    {
+        Ext<T> ext[ROWS];
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) ext[r] = Ext<T>::row(yr[r]);
+#pragma unroll
+        for (int n = ROWS / 2; n >= 1; n /= 2) {
+            const bool up = lane_col & (PER * n);
+#pragma unroll
+            for (int r = 0; r < n; ++r) {
+                const Ext<T> give = up ? ext[r] : ext[r + n], keep = up ? ext[r + n] : ext[r];
+                ext[r] = keep.with(give.shfl(PER * n));
+            }
+        }
+#pragma unroll
+        for (int o = PER / 2; o >= 1; o /= 2) ext[0] = ext[0].with(ext[0].shfl(o));
+        const uint32_t bits = grid_bits(make_grid(ext[0].mn(), ext[0].mx()));
+        const int mine = (lane_col % GL) / PER;  // these lanes' row
+        if (lane_col % PER == 0) {
+            uint16_t *vs = reinterpret_cast<uint16_t *>(rec + P::kPart + P::kGridOff);
+            const int at = (col / 64) * kChunk + slot + mine * NSLOT;
+            vs[at] = (uint16_t)bits;
+            vs[D + at] = (uint16_t)(bits >> 16);
+        }
+        const int lane0 = (tid & 31) & ~(GL - 1);
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) vgrid[r] = __shfl_sync(0xffffffffu, bits, lane0 + PER * r);
+    }
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
-        float sum = 0.f, mn = y[r][0], mx = y[r][0];
+        float y[VEC];
+        widen(yr[r], y);
+        const Grid g = grid_of(vgrid[r]);
+        const float inv = grid_inv(g.s);
+        float zs[VEC], iv[VEC], ss[VEC];
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-            sum += y[r][e];
-            mn = fminf(mn, y[r][e]);
-            mx = fmaxf(mx, y[r][e]);
-        }
-#pragma unroll
-        for (int o = GL / 2; o; o >>= 1) {
-            sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        }
-        const Grid g = make_grid(mn, mx, sum);
-        const float inv = grid_inv(g);
-        const int row = slot + r * NSLOT;
-        if (lane_col % GL == 0) {
-            vs[(col / 64) * kChunk + row] = bf16_bits(g.s);
-            vs[D + (col / 64) * kChunk + row] = bf16_bits(g.z);
+            zs[e] = g.z;
+            iv[e] = inv;
+            ss[e] = g.s;
         }
 #pragma unroll
         for (int e = 0; e < VEC; e += 4) {
-            uint32_t w = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w |= code_of(y[r][e + i], g, inv) << (8 * i);
-            *reinterpret_cast<uint32_t *>(vcodes + row * CS + col + e) = w;
+            const float (&x4)[4] = reinterpret_cast<const float (&)[4]>(y[e]);
+            const float (&s4)[4] = reinterpret_cast<const float (&)[4]>(ss[e]);
+            const float (&z4)[4] = reinterpret_cast<const float (&)[4]>(zs[e]);
+            const float (&i4)[4] = reinterpret_cast<const float (&)[4]>(iv[e]);
+            float d[4];
+            uint32_t w = codes<4, false>(x4, s4, z4, i4, d);
+            if (fmaxf(fmaxf(fabsf(d[0]), fabsf(d[1])), fmaxf(fabsf(d[2]), fabsf(d[3]))) > 0.5f * g.s)
+                w = exact_bytes(x4[0], x4[1], x4[2], x4[3], vgrid[r], w);
+            *reinterpret_cast<uint32_t *>(vcodes + (slot + r * NSLOT) * CS + col + e) = w;
         }
     }
     __syncthreads();
-
-    // K codes: a word holds the channels of one thread (bf16) or of a lane pair (fp32)
-    uint32_t kw[ROWS];
+    if (tid < D) {
+        float sum = 0.f;
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) kw[r] = 0;
+        for (int s = 0; s < NSLOT; ++s) sum += part_sum[s][tid];
+        if (summ) summ[(slice * summ_cap + first_chunk + j) * D + tid] = sum / (float)kChunk;
+    } else if (tid < D + WPR) {
+        const int w = tid - D;
+        uint32_t mn = part_mn[0][w], mx = part_mx[0][w];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-        const Grid g = kgrid[col + e];
-        const float inv = grid_inv(g);
-        const int el = (col + e) & 7;
-        const int sh = 4 * (el >> 1) + 16 * (el & 1);
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r) kw[r] |= code_of(x[r][e], g, inv) << sh;
-    }
-    uint32_t *kcodes = reinterpret_cast<uint32_t *>(rec);
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-        if (VEC == 4) kw[r] |= __shfl_xor_sync(0xffffffffu, kw[r], 1);
-        if (VEC == 8 || (lane_col & 1) == 0) kcodes[(slot + r * NSLOT) * (D / 8) + col / 8] = kw[r];
+        for (int s = 1; s < NSLOT; ++s) {
+            mn = word_min<T>(mn, part_mn[s][w]);
+            mx = word_max<T>(mx, part_mx[s][w]);
+        }
+        uint16_t *gs = reinterpret_cast<uint16_t *>(rec + P::kGridOff);
+        if constexpr (VEC == 8) {
+            const uint32_t g0 = grid_bits(make_grid(__uint_as_float(mn << 16), __uint_as_float(mx << 16)));
+            const uint32_t g1 =
+                grid_bits(make_grid(__uint_as_float(mn & 0xFFFF0000u), __uint_as_float(mx & 0xFFFF0000u)));
+            *reinterpret_cast<uint2 *>(&kgrid[2 * w]) = make_uint2(g0, g1);
+            *reinterpret_cast<uint32_t *>(gs + 2 * w) = __byte_perm(g0, g1, 0x5410);
+            *reinterpret_cast<uint32_t *>(gs + D + 2 * w) = __byte_perm(g0, g1, 0x7632);
+        } else {
+            const uint32_t g = grid_bits(make_grid(__uint_as_float(mn), __uint_as_float(mx)));
+            kgrid[w] = g;
+            gs[w] = (uint16_t)g;
+            gs[D + w] = (uint16_t)(g >> 16);
+        }
     }
 
     // V codes: four channels x eight tokens per step, turned in registers
@@ -193,6 +365,33 @@ __global__ void __launch_bounds__(kThreads) pack_kernel(const T *__restrict__ k,
         vw[(4 * c4 + 1) * 8 + w] = __byte_perm(lo01, lo23, 0x7632);
         vw[(4 * c4 + 2) * 8 + w] = __byte_perm(hi01, hi23, 0x5410);
         vw[(4 * c4 + 3) * 8 + w] = __byte_perm(hi01, hi23, 0x7632);
+    }
+    __syncthreads();
+
+    // K codes: a word holds the channels of one thread (bf16) or of a lane pair (fp32)
+    float ss[VEC], zs[VEC], iv[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+        const Grid g = grid_of(kgrid[col + e]);
+        ss[e] = g.s;
+        zs[e] = g.z;
+        iv[e] = grid_inv(g.s);
+    }
+    uint32_t *kcodes = reinterpret_cast<uint32_t *>(rec);
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        float x[VEC], d[VEC];
+        widen(xr[r], x);
+        uint32_t w = codes<VEC, true>(x, ss, zs, iv, d);
+        float far = -1.f;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) far = fmaxf(far, fmaf(-0.5f, ss[e], fabsf(d[e])));
+        if (far > 0.f) w = exact_nibbles<T>(xr[r], &kgrid[col], w);
+        if constexpr (VEC == 4) {  // elements 4 .. 7 of a word: pairs 2, 3
+            w <<= 8 * (lane_col & 1);
+            w |= __shfl_xor_sync(0xffffffffu, w, 1);
+        }
+        if (VEC == 8 || (lane_col & 1) == 0) kcodes[(slot + r * NSLOT) * (D / 8) + col / 8] = w;
     }
 }
 

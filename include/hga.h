@@ -627,10 +627,10 @@ hga_status_t hga_qk_norm_rope_bwd(const hga_proj_t *p, const void *q, const void
  * stands for bf16(s (16 + c) + z), rounded once.  For a group (one pair's elements)
  * with extremes mn, mx:
  *   s = bf16(fl32(fl32(mx - mn) / 15)), 0 if below 2^-100;  z = bf16(fl32(mn - 16 s));
- *   c = the code nearest to the element, (x - z) / s - 16 rounded to even in 0 .. 15.
+ *   c = the code nearest to the element, fl32(x - z) / s - 16 rounded to even in 0 .. 15.
  * So a value is off by at most half a step s/2, the roundings of z and of the value
  * (2^-9 |z| and 2^-9 |value|) and, at the ends, the range that rounding s lost.  A group
- * whose sum is not finite (a NaN or an infinity in it) reads back as NaN.
+ * with an element that is not finite (or whose s or z overflows) reads back as NaN.
  *   hist: device, 16-byte aligned, [B][Hkv][hist_cap_chunks] records.
  * The attention calls below attend exactly the values that hga_unpack_history
  * returns; a backward pass (or any other call of this header) over packed history

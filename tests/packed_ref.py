@@ -71,7 +71,8 @@ def quant(x, axis):
         z = to_bf16((mn - 16 * s).astype(np.float32).astype(np.float64))
         bad = ~np.isfinite(x).all(axis, keepdims=True) | ~np.isfinite(s) | ~np.isfinite(z)
         s, z = np.where(bad, np.nan, s), np.where(bad, np.nan, z)
-        c = np.clip(np.rint((x - z) / np.where(s == 0, 1.0, s)), 16, 31) - 16
+        y = (x - z).astype(np.float32).astype(np.float64)  # rounded to fp32
+        c = np.clip(np.rint(y / np.where(s == 0, 1.0, s)), 16, 31) - 16
         c = np.where((s == 0) | bad, 0, c).astype(np.int64)
     return s, z, c
 

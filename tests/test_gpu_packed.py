@@ -140,6 +140,27 @@ def test_extreme_groups(D, dtype):
             assert np.all((abs(t - t2) <= bound) | ~np.isfinite(s))
 
 
+@pytest.mark.parametrize("offset", [0.0, 3.0, 1000.0])
+def test_values_next_to_the_borders_between_codes(offset):
+    """fp32 values at, and 1 to 2^12 steps of fp32 to either side of, every border of grids with
+    steps of 8 significant bits; far offsets, whose z is rounded by more than a step, too."""
+    import hierarchical_sparse_long_b200 as hga
+    rng = np.random.default_rng(5)
+    D, n = 128, 3
+    k, v = np.empty((1, 1, n * 64, D), np.float32), np.empty((1, 1, n * 64, D), np.float32)
+    for at in np.ndindex(n, D):  # a channel of a chunk is a group of K
+        step = np.float32(rng.integers(128, 256)) * np.float32(2.0) ** -9
+        x = (rng.integers(0, 15, 64) + np.float32(0.5)).astype(np.float32) * step + np.float32(offset)
+        x = (x.view(np.int32) + rng.choice([0, 1, -1, 3, -17, 4096, -4096], 64).astype(np.int32)).view(np.float32)
+        x[0], x[1] = offset, offset + 15 * step
+        k[0, 0, 64 * at[0]:64 * at[0] + 64, at[1]] = x
+        v[0, 0, 64 * at[0] + at[1] % 64, 64 * (at[1] // 64):64 * (at[1] // 64) + 64] = x
+    hist = torch.zeros(1, 1, n, 72 * D, device="cuda", dtype=torch.uint8)
+    k, v = host(k, torch.float32), host(v, torch.float32)
+    hga.hga_pack_history(k, v, n * 64, 1, 1, D, 0, n, hist, n)
+    assert np.array_equal(hist.cpu().numpy(), ref.pack(f64(k), f64(v))[0])
+
+
 # ------------------------------------------------------------------ attention
 class Packed:
     """A packed history of random chunks, its values in 64 bits and a bf16 window or segment."""
