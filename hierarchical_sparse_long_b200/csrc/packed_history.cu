@@ -91,9 +91,8 @@ __device__ __forceinline__ uint32_t codes(const float (&x)[N], const float (&ss)
         const float2 y = __fadd2_rn(make_float2(x[e], x[e + 1]), make_float2(-zs[e], -zs[e + 1]));
         const float2 p = make_float2(__saturatef(fmaf(y.x, inv[e], -16.f / 15.f)),
                                      __saturatef(fmaf(y.y, inv[e + 1], -16.f / 15.f)));
-        const float2 u = __fadd2_rn(__ffma2_rn(p, make_float2(15.f, 15.f), make_float2(magic14, magic14)),
-                                    make_float2(-magic14, -magic14));
-        const float2 t = __fadd2_rn(u, make_float2(magic, magic));
+        const float2 u = __ffma2_rn(p, make_float2(15.f, 15.f), make_float2(magic14, magic14));
+        const float2 t = __fadd2_rn(u, make_float2(magic - magic14, magic - magic14));
         const float2 k = __fadd2_rn(t, make_float2(16.f - magic, 16.f - magic));
         const float2 d = __ffma2_rn(k, make_float2(-ss[e], -ss[e + 1]), y);
         r[e] = d.x;
@@ -195,7 +194,7 @@ template <typename T> __device__ __forceinline__ uint32_t word_max(uint32_t a, u
 // Thread (col, slot) owns VEC channels of the rows slot, slot + NSLOT, ...: the split of
 // summaries_kernel, whose sums are repeated here in the same order bit for bit.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 3) pack_kernel(const T *__restrict__ k, const T *__restrict__ v,
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) pack_kernel(const T *__restrict__ k, const T *__restrict__ v,
                                                         long long head_stride, int n_chunks, int first_chunk,
                                                         uint8_t *__restrict__ hist, long long cap,
                                                         float *__restrict__ summ, long long summ_cap) {
@@ -209,6 +208,7 @@ __global__ void __launch_bounds__(kThreads, 3) pack_kernel(const T *__restrict__
     __shared__ __align__(16) float part_sum[NSLOT][D + 4];
     __shared__ __align__(16) uint32_t part_mn[NSLOT][WPR + 4], part_mx[NSLOT][WPR + 4];
     __shared__ __align__(16) uint32_t kgrid[D];
+    __shared__ __align__(16) float kinv[D];
     __shared__ __align__(16) uint8_t vcodes[kChunk * CS];
     const int tid = threadIdx.x;
     const long long slice = blockIdx.x / n_chunks;
@@ -267,6 +267,7 @@ __global__ void __launch_bounds__(kThreads, 3) pack_kernel(const T *__restrict__
     constexpr int PER = GL / ROWS;  // lanes that end up with the same row
     static_assert(PER >= 1, "a row's lanes outnumber the rows of a thread");
     uint32_t vgrid[ROWS];
+    float vinv[ROWS];
     {
         Ext<T> ext[ROWS];
 #pragma unroll
@@ -283,6 +284,7 @@ __global__ void __launch_bounds__(kThreads, 3) pack_kernel(const T *__restrict__
 #pragma unroll
         for (int o = PER / 2; o >= 1; o /= 2) ext[0] = ext[0].with(ext[0].shfl(o));
         const uint32_t bits = grid_bits(make_grid(ext[0].mn(), ext[0].mx()));
+        const float own_inv = grid_inv(grid_of(bits).s);
         const int mine = (lane_col % GL) / PER;  // these lanes' row
         if (lane_col % PER == 0) {
             uint16_t *vs = reinterpret_cast<uint16_t *>(rec + P::kPart + P::kGridOff);
@@ -292,19 +294,21 @@ __global__ void __launch_bounds__(kThreads, 3) pack_kernel(const T *__restrict__
         }
         const int lane0 = (tid & 31) & ~(GL - 1);
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r) vgrid[r] = __shfl_sync(0xffffffffu, bits, lane0 + PER * r);
+        for (int r = 0; r < ROWS; ++r) {
+            vgrid[r] = __shfl_sync(0xffffffffu, bits, lane0 + PER * r);
+            vinv[r] = __shfl_sync(0xffffffffu, own_inv, lane0 + PER * r);
+        }
     }
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
         float y[VEC];
         widen(yr[r], y);
         const Grid g = grid_of(vgrid[r]);
-        const float inv = grid_inv(g.s);
         float zs[VEC], iv[VEC], ss[VEC];
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             zs[e] = g.z;
-            iv[e] = inv;
+            iv[e] = vinv[r];
             ss[e] = g.s;
         }
 #pragma unroll
@@ -340,11 +344,13 @@ __global__ void __launch_bounds__(kThreads, 3) pack_kernel(const T *__restrict__
             const uint32_t g1 =
                 grid_bits(make_grid(__uint_as_float(mn & 0xFFFF0000u), __uint_as_float(mx & 0xFFFF0000u)));
             *reinterpret_cast<uint2 *>(&kgrid[2 * w]) = make_uint2(g0, g1);
+            *reinterpret_cast<float2 *>(&kinv[2 * w]) = make_float2(grid_inv(grid_of(g0).s), grid_inv(grid_of(g1).s));
             *reinterpret_cast<uint32_t *>(gs + 2 * w) = __byte_perm(g0, g1, 0x5410);
             *reinterpret_cast<uint32_t *>(gs + D + 2 * w) = __byte_perm(g0, g1, 0x7632);
         } else {
             const uint32_t g = grid_bits(make_grid(__uint_as_float(mn), __uint_as_float(mx)));
             kgrid[w] = g;
+            kinv[w] = grid_inv(grid_of(g).s);
             gs[w] = (uint16_t)g;
             gs[D + w] = (uint16_t)(g >> 16);
         }
@@ -375,18 +381,29 @@ __global__ void __launch_bounds__(kThreads, 3) pack_kernel(const T *__restrict__
         const Grid g = grid_of(kgrid[col + e]);
         ss[e] = g.s;
         zs[e] = g.z;
-        iv[e] = grid_inv(g.s);
+        iv[e] = kinv[col + e];
     }
     uint32_t *kcodes = reinterpret_cast<uint32_t *>(rec);
+    uint32_t kw[ROWS];
+    float far[VEC];
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
         float x[VEC], d[VEC];
         widen(xr[r], x);
-        uint32_t w = codes<VEC, true>(x, ss, zs, iv, d);
-        float far = -1.f;
+        kw[r] = codes<VEC, true>(x, ss, zs, iv, d);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) far = fmaxf(far, fmaf(-0.5f, ss[e], fabsf(d[e])));
-        if (far > 0.f) w = exact_nibbles<T>(xr[r], &kgrid[col], w);
+        for (int e = 0; e < VEC; ++e) far[e] = r ? fmaxf(far[e], fabsf(d[e])) : fabsf(d[e]);
+    }
+    bool redo = false;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) redo |= far[e] > 0.5f * ss[e];
+    if (redo) {
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) kw[r] = exact_nibbles<T>(xr[r], &kgrid[col], kw[r]);
+    }
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        uint32_t w = kw[r];
         if constexpr (VEC == 4) {  // elements 4 .. 7 of a word: pairs 2, 3
             w <<= 8 * (lane_col & 1);
             w |= __shfl_xor_sync(0xffffffffu, w, 1);
