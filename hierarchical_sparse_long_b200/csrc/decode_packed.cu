@@ -6,11 +6,12 @@
 // them: z_t = q . k_t / sqrt(D), out = sum_t softmax(z)_t v_t.
 //
 // Bound by HBM, and at small batches by latency: a routed chunk is 72 D bytes (0.28 of
-// bf16), read once for the G <= 8 query heads of its KV head.  The codes go from global
-// memory straight into MMA operands, without shared memory: a warp takes a whole chunk,
-// and the axes that the products contract or run along are permuted so that a lane's
-// 16 (K) or 8 (V) bytes of a row are exactly its operand registers.  With lane = 4 r + c
-// (r = lane / 4, c = lane % 4):
+// bf16), read once for the G <= 8 query heads of its KV head.  A warp takes a whole chunk.
+// Its record comes as one bulk copy into the warp's own two-stage ring in shared memory, so
+// the next record is on its way while this one is multiplied, and no register holds data in
+// flight.  From there the codes are widened straight into MMA operands: the axes that the
+// products contract or run along are permuted so that a lane's 16 (K) or 8 (V) bytes of a
+// row are exactly its operand registers.  With lane = 4 r + c (r = lane / 4, c = lane % 4):
 //   S^T = K Q^T   M = 16 tokens, N = 8 heads.  Row r of token tile t is token
 //                 16 (r / 2) + 2 t + r % 2; lane c holds channels c D/4 .. + D/4, which
 //                 the k index runs through two pairs at a time (the queries likewise).
@@ -18,12 +19,14 @@
 //                 (D/4) (r / 2) + 2 u + r % 2; lane c holds tokens 16 c .. + 16.  P, as
 //                 S^T leaves it (tokens by heads), becomes that operand by one
 //                 transposing move per 8 tokens.
-// The tokens of the window go through the same products in pieces of 16, read as bf16.
+// The tokens of the window go through the same ring and products in pieces of 16, as bf16.
 //
 // The units (routed chunks, then window pieces) of one (batch, KV head) are dealt to the
 // warps of a thread-block cluster; every warp keeps its own running maximum, sum and
 // output, which are merged through shared memory, first of the CTA, then of the
 // cluster: one launch, no workspace, sums in a fixed order.
+#include <cstddef>
+
 #include "packed.cuh"
 #include "tc_ptx.cuh"
 
@@ -38,7 +41,8 @@ constexpr int kPiece = 16;      // window tokens per unit
 constexpr int kMaxRouted = 64;  // topk limit of the parameter check
 constexpr int kHeads = 8;       // query heads per KV head: the N side of the products
 constexpr int kMaxCluster = 8;  // portable cluster size
-constexpr int kCtasPerSm = 2;
+constexpr int kCtasPerSm = 3;   // 168 registers a thread, 74 KiB of rings a CTA
+constexpr int kStages = 2;      // one unit multiplied, one on its way
 
 struct PackedDecodeArgs {
     const __nv_bfloat16 *q;
@@ -51,6 +55,7 @@ struct PackedDecodeArgs {
     unsigned *status;
     long long cap, local_stride;
     int n_q_heads, n_kv_heads, topk, n_hist_chunks, n_local, n_cluster;
+    int merge_groups, merge_shift;  // groups of four outputs per CTA, log2 of the lanes of one
     float scale_log2;  // log2(e) / sqrt(D)
 };
 
@@ -61,34 +66,50 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return y;
 }
 
-// N bytes (a multiple of 8) of read-once data.
+// N bytes (a multiple of 8) of a ring stage.
 template <int N> __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[N / 4]) {
 #pragma unroll
     for (int i = 0; i < N / 16; ++i) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+        const uint4 v = *(reinterpret_cast<const uint4 *>(p) + i);
         w[4 * i] = v.x;
         w[4 * i + 1] = v.y;
         w[4 * i + 2] = v.z;
         w[4 * i + 3] = v.w;
     }
     if constexpr (N % 16 == 8) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p + N / 16 * 16));
+        const uint2 v = *reinterpret_cast<const uint2 *>(p + N / 16 * 16);
         w[N / 4 - 2] = v.x;
         w[N / 4 - 1] = v.y;
     }
 }
+
+// 16 bytes of shared memory of the cluster.
+__device__ __forceinline__ float4 load_peer(uint32_t addr) {
+    const uint4 v = tc::ld_dsmem_v4(addr);
+    return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+}
+
+// Partial results of a CTA's warps: maximum and sum by head, outputs in quarters of a row
+// with pads that spread a warp's stores over the banks.
+template <int D> struct Merge {
+    static constexpr int kQuarter = D / 4 + 4, kRow = 4 * kQuarter + 4;
+    float4 m[kHeads], l[kHeads];  // of the four warps
+    float o[kWarps][kHeads][kRow];
+};
+static_assert(kWarps == 4, "a head's maxima of a CTA are one float4");
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_packed_kernel(const PackedDecodeArgs a) {
     using P = Packed<D>;
     constexpr int NJ = D / 32;  // channel octets of a lane
     constexpr int NU = D / 8;   // 8-channel row tiles
-    __shared__ int units[kMaxRouted];
-    __shared__ int n_routed;
-    __shared__ float wm[kWarps][kHeads], wl[kWarps][kHeads];
-    __shared__ __align__(16) float wo[kWarps][kHeads][D + 4];
-    __shared__ float cm[kHeads], cl[kHeads];        // the CTA's merged maximum and sum
-    __shared__ __align__(16) float co[kHeads][D];   // and output
+    static_assert(4 * kPiece * D <= P::kRecord, "a window piece fits a ring stage");
+    using M = Merge<D>;
+    static_assert(sizeof(M) <= kWarps * kStages * P::kRecord, "the merge reuses the rings");
+    extern __shared__ __align__(16) uint8_t rings[];  // [kWarps][kStages][record]
+    __shared__ int units[kWarps][kMaxRouted];
+    __shared__ uint64_t full[kWarps][kStages];
+    __shared__ int abort_flag;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int r = lane >> 2, c = lane & 3;
@@ -96,21 +117,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_packed_kernel(con
     const int rank = (int)blockIdx.x % a.n_cluster;
     const int bg = (int)blockIdx.x / a.n_cluster;
     const int b = bg / a.n_kv_heads, g = bg % a.n_kv_heads;
-
-    if (warp == 0) {  // the valid routes, in order; -1 is padding, anything else out of range is skipped
-        const int32_t *sel = a.idx + (long long)bg * a.topk;
-        int n = 0;
-#pragma unroll
-        for (int i0 = 0; i0 < kMaxRouted; i0 += 32) {
-            const int j = i0 + lane < a.topk ? sel[i0 + lane] : -1;
-            const bool ok = j >= 0 && j < a.n_hist_chunks;
-            if (!ok && j != -1 && rank == 0) atomicOr(a.status, kDevBadIndex);
-            const unsigned m = __ballot_sync(0xffffffffu, ok);
-            if (ok) units[n + __popc(m & ((1u << lane) - 1u))] = j;
-            n += __popc(m);
-        }
-        if (lane == 0) n_routed = n;
-    }
 
     // queries of head r as the B operand: pair p of octet j of the lane's channels
     uint32_t qf[NJ][4];
@@ -125,6 +131,49 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_packed_kernel(con
         qf[j][2] = v.z;
         qf[j][3] = v.w;
     }
+    if (tid == 0) abort_flag = 0;
+    if (lane == 0) {
+        for (int s = 0; s < kStages; ++s) tc::mbar_init(&full[warp][s], 1);
+        tc::fence_mbar_init();
+    }
+    int nr = 0;
+    {  // the valid routes, in order; -1 is padding, anything else out of range is skipped
+        const int32_t *sel = a.idx + (long long)bg * a.topk;
+#pragma unroll
+        for (int i0 = 0; i0 < kMaxRouted; i0 += 32) {
+            const int j = i0 + lane < a.topk ? sel[i0 + lane] : -1;
+            const bool ok = j >= 0 && j < a.n_hist_chunks;
+            if (!ok && j != -1 && rank == 0 && warp == 0) atomicOr(a.status, kDevBadIndex);
+            const unsigned m = __ballot_sync(0xffffffffu, ok);
+            if (ok) units[warp][nr + __popc(m & ((1u << lane) - 1u))] = j;
+            nr += __popc(m);
+        }
+    }
+    __syncwarp();
+    const int n_units = nr + (a.n_local + kPiece - 1) / kPiece;
+    const int step = a.n_cluster * kWarps;
+    // a warp's units interleave over the CTAs first, so that few units use every SM
+    const int u0 = warp * a.n_cluster + rank;
+    uint8_t *ring = rings + warp * kStages * P::kRecord;
+    // unit u into stage s: a record, or a window piece's K rows and V rows
+    auto fetch = [&](int u, int s) {
+        if (lane != 0) return;
+        uint8_t *dst = ring + s * P::kRecord;
+        if (u < nr) {
+            tc::mbar_arrive_expect_tx(&full[warp][s], P::kRecord);
+            tc::bulk_load(dst, a.hist + ((long long)bg * a.cap + units[warp][u]) * P::kRecord, P::kRecord,
+                          &full[warp][s]);
+        } else {
+            const int t0 = (u - nr) * kPiece;
+            const int n = a.n_local - t0 < kPiece ? a.n_local - t0 : kPiece;
+            const long long row0 = (long long)bg * a.local_stride + t0;
+            tc::mbar_arrive_expect_tx(&full[warp][s], 4 * n * D);
+            tc::bulk_load(dst, a.kl + row0 * D, 2 * n * D, &full[warp][s]);
+            tc::bulk_load(dst + 2 * kPiece * D, a.vl + row0 * D, 2 * n * D, &full[warp][s]);
+        }
+    };
+    if (u0 < n_units) fetch(u0, 0);
+
     // state of heads 2c, 2c + 1: o[i] rows r (channel tile 2i) and r + 8 (tile 2i + 1)
     float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};  // l: this lane's tokens only
     float o[NU / 2][4];
@@ -132,13 +181,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_packed_kernel(con
     for (int i = 0; i < NU / 2; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-    __syncthreads();
-
-    const int nr = n_routed;
-    const int n_units = nr + (a.n_local + kPiece - 1) / kPiece;
-    const int step = a.n_cluster * kWarps;
-    // a warp's units interleave over the CTAs first, so that few units use every SM
-    int u = warp * a.n_cluster + rank;
+    __syncthreads();  // abort_flag
 
     // one online-softmax step over NT tiles of 16 tokens: s holds raw scores of (token
     // rows r, r + 8; heads 2c, 2c + 1), -inf where masked; leaves P^T operands in pt
@@ -181,8 +224,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_packed_kernel(con
         }
     };
 
-    for (; u < nr; u += step) {
-        const uint8_t *rec = a.hist + ((long long)bg * a.cap + units[u]) * P::kRecord;
+    auto chunk = [&](const uint8_t *rec) {
         const uint8_t *vrec = rec + P::kPart;
         uint32_t kw[8][NJ], vw[NU][2];
 #pragma unroll
@@ -234,14 +276,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_packed_kernel(con
                 tc::mma_16816(o[i], f1, pt[4 * w + 2], pt[4 * w + 3]);
             }
         }
-    }
+    };
 
-    for (; u < n_units; u += step) {  // window pieces of 16 tokens; rows past n_local read as zeros
-        const int t0 = (u - nr) * kPiece;
-        const int left = a.n_local - t0;
-        const long long row0 = (long long)bg * a.local_stride + t0;
-        const uint8_t *kp = reinterpret_cast<const uint8_t *>(a.kl + row0 * D);
-        const uint8_t *vp = reinterpret_cast<const uint8_t *>(a.vl + row0 * D);
+    // a window piece of 16 tokens, `left` of them in the window: rows past that read as zeros
+    auto piece = [&](const uint8_t *kp, int left) {
+        const uint8_t *vp = kp + 2 * kPiece * D;
         uint32_t kx[2][NJ][4], vx[2][NJ][4];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -276,77 +315,101 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_packed_kernel(con
                                    transpose8(vx[1][j][e + 1])};
             tc::mma_16816(o[i], f, pt[0], pt[1]);
         }
+    };
+
+    bool ok = true;
+    for (int u = u0, i = 0; ok && u < n_units; u += step, ++i) {
+        uint64_t *bar = &full[warp][i & 1];
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(bar, (i >> 1) & 1, &abort_flag, a.status));
+        if (!ok) {  // the copy still lands before the ring is used again
+            int never = 0;
+            tc::mbar_wait(bar, (i >> 1) & 1, &never, a.status, 1ll << 28);
+            break;
+        }
+        // the next unit, into the stage that the previous one left: not before this one has
+        // arrived, so that the first units of all warps share the bandwidth of the start
+        if (u + step < n_units) fetch(u + step, (i + 1) & 1);
+        const uint8_t *rec = ring + (i & 1) * P::kRecord;
+        if (u < nr) {
+            chunk(rec);
+        } else {
+            piece(rec, a.n_local - (u - nr) * kPiece);
+        }
+        __syncwarp();  // every lane has read the stage
     }
+    __syncthreads();  // the rings are free
 
     // this warp's maximum, sum and output
+    M &mg = *reinterpret_cast<M *>(rings);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l_run[h] += __shfl_xor_sync(0xffffffffu, l_run[h], d);
         if (r == 0) {
-            wm[warp][2 * c + h] = m_run[h];
-            wl[warp][2 * c + h] = l_run[h];
+            reinterpret_cast<float *>(&mg.m[2 * c + h])[warp] = m_run[h];
+            reinterpret_cast<float *>(&mg.l[2 * c + h])[warp] = l_run[h];
         }
+        float *row = &mg.o[warp][2 * c + h][M::kQuarter * (r >> 1) + (r & 1)];
 #pragma unroll
         for (int i = 0; i < NU / 2; ++i) {
-            const int ch = (D / 4) * (r >> 1) + 4 * i + (r & 1);
-            wo[warp][2 * c + h][ch] = o[i][h];
-            wo[warp][2 * c + h][ch + 2] = o[i][2 + h];
+            row[4 * i] = o[i][h];
+            row[4 * i + 2] = o[i][2 + h];
         }
     }
-    __syncthreads();
-    // the CTA's: a warp without units has m = -inf and adds nothing
-    for (int e = tid; e < G * D; e += kThreads) {
-        const int h = e / D, d = e % D;
-        float m = wm[0][h];
+    // The sum over all warps of the cluster, in a fixed order.  Four outputs belong to kl
+    // lanes, one for each CTA (a power of two of them), which reads that CTA's four warps;
+    // the lanes' sums then meet in shuffles.  The groups of four are dealt evenly to the CTAs.
+    // A warp without units, and a lane past the cluster's end, has m = -inf and adds nothing.
+    const int nc = a.n_cluster, kl = 1 << a.merge_shift;
+    if (nc > 1) tc::cluster_arrive();
+    const int end = min((rank + 1) * a.merge_groups, G * D / 4);
+    const int k = tid & (kl - 1);
+    int e0 = rank * a.merge_groups;
+    if (nc > 1)
+        tc::cluster_wait();
+    else
+        __syncthreads();
+#pragma unroll 1
+    for (; e0 < end; e0 += kThreads >> a.merge_shift) {
+        const int e = min(e0 + (tid >> a.merge_shift), end - 1);
+        const int h = e / (D / 4), d4 = e % (D / 4);
+        float4 mv = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY), lv = make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 ov[kWarps] = {lv, lv, lv, lv};
+        if (k < nc) {
+            const uint32_t sm = tc::mapa_shared(tc::smem_u32(&mg), k);
+            mv = load_peer(sm + (uint32_t)offsetof(M, m) + 16 * h);
+            lv = load_peer(sm + (uint32_t)offsetof(M, l) + 16 * h);
+            const uint32_t at = 4 * (h * M::kRow + M::kQuarter * (d4 / (D / 16)) + 4 * (d4 % (D / 16)));
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) m = fmaxf(m, wm[w][h]);
+            for (int w = 0; w < kWarps; ++w)
+                ov[w] = load_peer(sm + (uint32_t)offsetof(M, o) + w * (uint32_t)sizeof(mg.o[0]) + at);
+        }
+        float m = fmaxf(fmaxf(mv.x, mv.y), fmaxf(mv.z, mv.w));
+#pragma unroll 1
+        for (int o = kl / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         const float m_sub = m == -INFINITY ? 0.f : m;
-        float l = 0.f, acc = 0.f;
+        const float f[4] = {tc::ex2(mv.x - m_sub), tc::ex2(mv.y - m_sub), tc::ex2(mv.z - m_sub), tc::ex2(mv.w - m_sub)};
+        float v[5] = {lv.x * f[0] + lv.y * f[1] + lv.z * f[2] + lv.w * f[3], 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float f = exp2f(wm[w][h] - m_sub);
-            l = fmaf(wl[w][h], f, l);
-            acc = fmaf(wo[w][h][d], f, acc);
+            v[1] = fmaf(ov[w].x, f[w], v[1]);
+            v[2] = fmaf(ov[w].y, f[w], v[2]);
+            v[3] = fmaf(ov[w].z, f[w], v[3]);
+            v[4] = fmaf(ov[w].w, f[w], v[4]);
         }
-        if (a.n_cluster == 1) {
+#pragma unroll 1
+        for (int o = kl / 2; o; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < 5; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        if (k == 0 && e0 + (tid >> a.merge_shift) < end) {
             const long long row = (long long)b * a.n_q_heads + (long long)g * G + h;
-            a.out[row * D + d] = __float2bfloat16_rn(acc / l);
-            if (d == 0) a.lse[row] = (m + log2f(l)) * 0.69314718055994530942f;
-        } else {
-            co[h][d] = acc;
-            if (d == 0) {
-                cm[h] = m;
-                cl[h] = l;
-            }
+            const float inv = 1.f / v[0];
+            *reinterpret_cast<uint2 *>(a.out + row * D + 4 * d4) =
+                make_uint2(tc::pack_bf16(v[1] * inv, v[2] * inv), tc::pack_bf16(v[3] * inv, v[4] * inv));
+            if (d4 == 0) a.lse[row] = (m + log2f(v[0])) * 0.69314718055994530942f;
         }
     }
-    if (a.n_cluster == 1) return;
-    tc::cluster_arrive();
-    tc::cluster_wait();
-    // the cluster's: element e of the G x D outputs by CTA rank (e / kThreads) % n_cluster
-    const uint32_t sm = tc::smem_u32(cm), sl = tc::smem_u32(cl), so = tc::smem_u32(co);
-    for (int e = rank * kThreads + tid; e < G * D; e += a.n_cluster * kThreads) {
-        const int h = e / D, d = e % D;
-        float mv[kMaxCluster], m = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < kMaxCluster; ++k) {
-            mv[k] = k < a.n_cluster ? tc::ld_dsmem_f32(tc::mapa_shared(sm + 4 * h, k)) : -INFINITY;
-            m = fmaxf(m, mv[k]);
-        }
-        const float m_sub = m == -INFINITY ? 0.f : m;
-        float l = 0.f, acc = 0.f;
-#pragma unroll
-        for (int k = 0; k < kMaxCluster; ++k)
-            if (k < a.n_cluster) {
-                const float f = exp2f(mv[k] - m_sub);
-                l = fmaf(tc::ld_dsmem_f32(tc::mapa_shared(sl + 4 * h, k)), f, l);
-                acc = fmaf(tc::ld_dsmem_f32(tc::mapa_shared(so + 4 * (h * D + d), k)), f, acc);
-            }
-        const long long row = (long long)b * a.n_q_heads + (long long)g * G + h;
-        a.out[row * D + d] = __float2bfloat16_rn(acc / l);
-        if (d == 0) a.lse[row] = (m + log2f(l)) * 0.69314718055994530942f;
-    }
+    if (nc == 1) return;
     // no CTA leaves while another may read its shared memory
     tc::cluster_arrive();
     tc::cluster_wait();
@@ -374,7 +437,11 @@ template <int D> hga_status_t launch_d(const PackedDecodeArgs &a, unsigned bg, c
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, decode_packed_kernel<D>, a);
+    constexpr int smem = kWarps * kStages * Packed<D>::kRecord;
+    cfg.dynamicSmemBytes = smem;
+    cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(decode_packed_kernel<D>), smem);
+    if (e != cudaSuccess) return record_cuda(e);
+    e = cudaLaunchKernelEx(&cfg, decode_packed_kernel<D>, a);
     if (e == cudaSuccess) e = cudaGetLastError();
     return record_cuda(e);
 }
@@ -401,6 +468,8 @@ hga_status_t launch_decode_packed(const hga_params_t &p, const void *q, const ui
     a.n_hist_chunks = p.n_hist_chunks;
     a.n_local = n_local;
     a.n_cluster = cluster_size(p, n_local);
+    a.merge_groups = (p.n_q_heads / p.n_kv_heads * p.head_dim / 4 + a.n_cluster - 1) / a.n_cluster;
+    a.merge_shift = a.n_cluster == 1 ? 0 : a.n_cluster == 2 ? 1 : a.n_cluster <= 4 ? 2 : 3;
     a.scale_log2 = (float)(1.4426950408889634 / __builtin_sqrt((double)p.head_dim));
     const unsigned bg = (unsigned)(p.batch * p.n_kv_heads);
     return p.head_dim == 128 ? launch_d<128>(a, bg, stream) : launch_d<64>(a, bg, stream);

@@ -33,8 +33,9 @@ template <int D> struct Packed {
 // two elements' grids.
 template <int J> __device__ __forceinline__ uint32_t packed_pair(uint32_t w, uint32_t s, uint32_t z) {
     const uint32_t sh = J == 0 ? w << 3 : w >> (4 * J - 3);
-    const uint32_t m = (sh & 0x00780078u) | 0x41804180u;
-    uint32_t r;
+    uint32_t m, r;
+    // (sh & mask) | 16.0 pair: one instruction, with both constants in registers
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(m) : "r"(sh), "r"(0x00780078u), "r"(0x41804180u));
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(m), "r"(s), "r"(z));
     return r;
 }
