@@ -28,6 +28,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kHeads = 4;  // heads per thread of a long call
+constexpr int kBwdCtas = 3;  // CTAs per SM of the backward: 168 registers a thread
 
 struct NormRopeArgs {
     const void *x[3];  // q, k, v projections
@@ -47,24 +48,54 @@ struct NormRopeArgs {
     float eps;
 };
 
-template <typename T> __device__ __forceinline__ void store_vec(T *p, const float *v);
-template <> __device__ __forceinline__ void store_vec<float>(float *p, const float *v) {
-    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-}
-template <> __device__ __forceinline__ void store_vec<__nv_bfloat16>(__nv_bfloat16 *p, const float *v) {
-    uint4 u;
-    uint32_t *w = &u.x;
+// A 16-byte vector as pairs of fp32, the operands of the two-element instructions.
+template <typename T> struct Pairs {
+    static constexpr int N = Vec16<T>::N / 2;
+    float2 v[N];
+    __device__ __forceinline__ static Pairs widen(const uint4 &u) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        Pairs p;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t *>(&b);
+        for (int i = 0; i < N; ++i)
+            p.v[i] = sizeof(T) == 2 ? make_float2(__uint_as_float(w[i % 4] << 16), __uint_as_float(w[i % 4] & 0xFFFF0000u))
+                                    : make_float2(__uint_as_float(w[2 * i % 4]), __uint_as_float(w[(2 * i + 1) % 4]));
+        return p;
     }
-    *reinterpret_cast<uint4 *>(p) = u;
-}
-template <int N> __device__ __forceinline__ void load_f32(const float *p, float *v) {
+    __device__ __forceinline__ static Pairs fill(float x) {
+        Pairs p;
 #pragma unroll
-    for (int i = 0; i < N; i += 4) Vec16<float>::load(p + i, v + i);
-}
+        for (int i = 0; i < N; ++i) p.v[i] = make_float2(x, x);
+        return p;
+    }
+    __device__ __forceinline__ static Pairs load_f32(const float *src) {
+        Pairs p;
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            const float4 f = *reinterpret_cast<const float4 *>(src + 2 * i);
+            p.v[i] = make_float2(f.x, f.y);
+            p.v[i + 1] = make_float2(f.z, f.w);
+        }
+        return p;
+    }
+    // rounded to T
+    __device__ __forceinline__ void store(T *dst) const {
+        uint4 u;
+        uint32_t *w = &u.x;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if constexpr (sizeof(T) == 2) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(v[i].x, v[i].y);
+                w[i] = *reinterpret_cast<const uint32_t *>(&b);
+            } else {
+                w[2 * i] = __float_as_uint(v[i].x);
+                w[2 * i + 1] = __float_as_uint(v[i].y);
+            }
+        }
+        *reinterpret_cast<uint4 *>(dst) = u;
+    }
+};
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 minus(float2 x) { return make_float2(-x.x, -x.y); }
 
 // Sum over the L lanes of a row.
 template <int L> __device__ __forceinline__ float row_sum(float v) {
@@ -107,26 +138,39 @@ template <int VEC> __device__ __forceinline__ bool lane_vectors(const NormRopeAr
     return rotated;
 }
 
-template <int VEC>
-__device__ __forceinline__ void load_cs(const NormRopeArgs &a, long long pos, int e0, bool rotated, float *c,
-                                        float *s) {
+// cos, sin and -sin of a lane's pairs.
+template <typename T> struct Turn {
+    Pairs<T> c, s, ns;
+    __device__ __forceinline__ Turn(const NormRopeArgs &a, long long pos, int e0, bool rotated) {
+        c = Pairs<T>::fill(1.f);
+        s = Pairs<T>::fill(0.f);
+        if (rotated) {
+            const float *row = a.table + pos * a.rot + e0;
+            c = Pairs<T>::load_f32(row);
+            s = Pairs<T>::load_f32(row + a.rot / 2);
+        }
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-        c[e] = 1.f;
-        s[e] = 0.f;
+        for (int i = 0; i < Pairs<T>::N; ++i) ns.v[i] = minus(s.v[i]);
     }
-    if (rotated) {
-        const float *row = a.table + pos * a.rot + e0;
-        load_f32<VEC>(row, c);
-        load_f32<VEC>(row + a.rot / 2, s);
-    }
+};
+
+// 1 / sqrt(mean square + eps) of a row whose lane holds x0, x1.
+template <typename T, int D> __device__ __forceinline__ float rms(const Pairs<T> &x0, const Pairs<T> &x1, float eps) {
+    float2 sum = __fmul2_rn(x0.v[0], x0.v[0]);
+#pragma unroll
+    for (int i = 1; i < Pairs<T>::N; ++i) sum = __ffma2_rn(x0.v[i], x0.v[i], sum);
+#pragma unroll
+    for (int i = 0; i < Pairs<T>::N; ++i) sum = __ffma2_rn(x1.v[i], x1.v[i], sum);
+    return rsqrtf(row_sum<D / (2 * Vec16<T>::N)>(sum.x + sum.y) * (1.f / D) + eps);
 }
 
 // HPT heads of one token per thread group.  Long calls take four, whose loads are in
 // flight together and share the token's cos / sin and the weights; short ones take
-// one, so that a single token's heads spread over more SMs.
+// one, so that a single token's heads spread over more SMs.  The rows are asked for before
+// the position is known (a padding row's are read and dropped): one latency less.
 template <typename T, int D, int HPT>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeArgs a) {
+__global__ void __launch_bounds__(kThreads, HPT == 1 ? 8 : 5) norm_rope_kernel(const NormRopeArgs a) {
+    using Pr = Pairs<T>;
     constexpr int VEC = Vec16<T>::N;
     constexpr int L = D / (2 * VEC);  // lanes per row
     int h0;
@@ -136,60 +180,65 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeArgs 
     const long long n_tok = (long long)a.batch * a.seq_len;
     const long long t = (long long)blockIdx.x * (kThreads / L) + threadIdx.x / L;
     const bool live = t < n_tok;
-    const long long pos = live ? token_pos(a, t) : -1;
     int e0, e1;
     const bool rotated = lane_vectors<VEC>(a, l, e0, e1);
 
-    float x[HPT][2][VEC];
-    const T *src = static_cast<const T *>(a.x[kind]) + t * a.x_stride[kind];
+    uint4 x[HPT][2];
+    const T *src = static_cast<const T *>(a.x[kind]) + t * a.x_stride[kind] + h0 * D;
 #pragma unroll
-    for (int h = 0; h < HPT; ++h)
-        if (pos >= 0 && h0 + h < n_heads) {
-            Vec16<T>::load(src + (h0 + h) * D + e0, x[h][0]);
-            Vec16<T>::load(src + (h0 + h) * D + e1, x[h][1]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) x[h][0][e] = x[h][1][e] = 0.f;
-        }
-    const long long b = t / a.seq_len, i = t % a.seq_len;
-    const long long hs = kind == 0 ? a.seq_len : a.kv_stride;
-    T *dst = static_cast<T *>(a.y[kind]);
-    if (kind < 2) {
-        float w[2][VEC], c[VEC], s[VEC];
-        Vec16<T>::load(static_cast<const T *>(a.w[kind]) + e0, w[0]);
-        Vec16<T>::load(static_cast<const T *>(a.w[kind]) + e1, w[1]);
-        load_cs<VEC>(a, pos, e0, rotated && pos >= 0, c, s);
-#pragma unroll
-        for (int h = 0; h < HPT; ++h) {
-            float sum = 0.f;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) sum = fmaf(x[h][0][e], x[h][0][e], fmaf(x[h][1][e], x[h][1][e], sum));
-            const float r = rsqrtf(row_sum<L>(sum) * (1.f / D) + a.eps);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const float n0 = x[h][0][e] * r * w[0][e], n1 = x[h][1][e] * r * w[1][e];
-                x[h][0][e] = n0 * c[e] - n1 * s[e];
-                x[h][1][e] = n1 * c[e] + n0 * s[e];
-            }
+    for (int h = 0; h < HPT; ++h) {
+        x[h][0] = x[h][1] = make_uint4(0u, 0u, 0u, 0u);
+        if (live && h0 + h < n_heads) {
+            x[h][0] = *reinterpret_cast<const uint4 *>(src + h * D + e0);
+            x[h][1] = *reinterpret_cast<const uint4 *>(src + h * D + e1);
         }
     }
-    if (pos < 0) return;
+    const long long pos = live ? token_pos(a, t) : -1;
+    const long long b = t / a.seq_len, i = t % a.seq_len;
+    const long long hs = kind == 0 ? a.seq_len : a.kv_stride;
+    T *dst = static_cast<T *>(a.y[kind]) + ((b * n_heads + h0) * hs + i) * D;
+    if (kind == 2) {
+        if (pos < 0) return;
 #pragma unroll
-    for (int h = 0; h < HPT; ++h)
-        if (h0 + h < n_heads) {
-            T *row = dst + ((b * n_heads + h0 + h) * hs + i) * D;
-            store_vec<T>(row + e0, x[h][0]);
-            store_vec<T>(row + e1, x[h][1]);
+        for (int h = 0; h < HPT; ++h)
+            if (h0 + h < n_heads) {
+                *reinterpret_cast<uint4 *>(dst + h * hs * D + e0) = x[h][0];
+                *reinterpret_cast<uint4 *>(dst + h * hs * D + e1) = x[h][1];
+            }
+        return;
+    }
+    const T *wp = static_cast<const T *>(a.w[kind]);
+    const Pr w0 = Pr::widen(*reinterpret_cast<const uint4 *>(wp + e0));
+    const Pr w1 = Pr::widen(*reinterpret_cast<const uint4 *>(wp + e1));
+    const Turn<T> turn(a, pos, e0, rotated && pos >= 0);
+#pragma unroll
+    for (int h = 0; h < HPT; ++h) {
+        Pr x0 = Pr::widen(x[h][0]), x1 = Pr::widen(x[h][1]);
+        const float2 r = both(rms<T, D>(x0, x1, a.eps));
+#pragma unroll
+        for (int j = 0; j < Pr::N; ++j) {
+            const float2 n0 = __fmul2_rn(__fmul2_rn(x0.v[j], r), w0.v[j]);
+            const float2 n1 = __fmul2_rn(__fmul2_rn(x1.v[j], r), w1.v[j]);
+            x0.v[j] = __ffma2_rn(n1, turn.ns.v[j], __fmul2_rn(n0, turn.c.v[j]));
+            x1.v[j] = __ffma2_rn(n0, turn.s.v[j], __fmul2_rn(n1, turn.c.v[j]));
         }
+        if (pos >= 0 && h0 + h < n_heads) {
+            x0.store(dst + h * hs * D + e0);
+            x1.store(dst + h * hs * D + e1);
+        }
+    }
 }
 
 // Gradients: dx of each row, and per CTA the sum over its rows of dn xh, which
 // norm_rope_dw adds up in a fixed order (no atomics: the same inputs give the same bits).
+// Heads go in pairs, whose loads are in flight together; a head's are 96 bytes a lane.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const NormRopeArgs a) {
+__global__ void __launch_bounds__(kThreads, kBwdCtas) norm_rope_bwd_kernel(const NormRopeArgs a) {
+    using Pr = Pairs<T>;
     constexpr int VEC = Vec16<T>::N;
     constexpr int L = D / (2 * VEC);
     constexpr int SLOTS = kThreads / L;  // tokens at once
+    constexpr int HP = 2;
     __shared__ float part[SLOTS][D + 4];
     int h0;
     const int kind = cta_kind(a, kHeads, h0);
@@ -198,77 +247,83 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const NormRopeA
     const long long n_tok = (long long)a.batch * a.seq_len;
     int e0, e1;
     const bool rotated = lane_vectors<VEC>(a, l, e0, e1);
-    float w[2][VEC], dw[2][VEC];
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) dw[0][e] = dw[1][e] = 0.f;
+    // norm_rope_dw may take its place beside this kernel's last CTAs
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    Pr dw0 = Pr::fill(0.f), dw1 = dw0;
+    uint4 wr[2] = {};
     if (kind < 2) {
-        Vec16<T>::load(static_cast<const T *>(a.w[kind]) + e0, w[0]);
-        Vec16<T>::load(static_cast<const T *>(a.w[kind]) + e1, w[1]);
+        wr[0] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.w[kind]) + e0);
+        wr[1] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.w[kind]) + e1);
     }
     // every lane of a warp takes the same number of steps: the row sums are warp-wide
     for (long long t0 = (long long)blockIdx.x * SLOTS; t0 < n_tok; t0 += (long long)gridDim.x * SLOTS) {
         const long long t = t0 + slot;
         const bool live = t < n_tok;
-        const long long pos = live ? token_pos(a, t) : -1;
         const long long b = t / a.seq_len, i = t % a.seq_len;
-        const T *src = static_cast<const T *>(a.x[kind]) + t * a.x_stride[kind];
-        T *dst = static_cast<T *>(a.dx[kind]) + t * a.x_stride[kind];
-        float c[VEC], s[VEC];
-        if (kind < 2) load_cs<VEC>(a, pos, e0, rotated && pos >= 0, c, s);
+        const T *src = static_cast<const T *>(a.x[kind]) + t * a.x_stride[kind] + h0 * D;
+        T *dst = static_cast<T *>(a.dx[kind]) + t * a.x_stride[kind] + h0 * D;
+        const float *dy = a.dy[kind] + ((b * n_heads + h0) * (long long)a.seq_len + i) * D;
+        const long long dy_head = (long long)a.seq_len * D;
+        const long long pos = live ? token_pos(a, t) : -1;
+        const Turn<T> turn(a, pos, e0, kind < 2 && rotated && pos >= 0);
 #pragma unroll
-        for (int h = 0; h < kHeads; ++h) {
-            const bool on = pos >= 0 && h0 + h < n_heads;
-            float g[2][VEC];
+        for (int hp = 0; hp < kHeads; hp += HP) {
+            if (h0 + hp >= n_heads) break;
+            Pr g0[HP], g1[HP];
+            uint4 x[HP][2];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) g[0][e] = g[1][e] = 0.f;
-            if (on) {
-                const float *row = a.dy[kind] + ((b * n_heads + h0 + h) * (long long)a.seq_len + i) * D;
-                load_f32<VEC>(row + e0, g[0]);
-                load_f32<VEC>(row + e1, g[1]);
-            }
-            if (kind < 2) {
-                float x[2][VEC];
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) x[0][e] = x[1][e] = 0.f;
-                if (on) {
-                    Vec16<T>::load(src + (h0 + h) * D + e0, x[0]);
-                    Vec16<T>::load(src + (h0 + h) * D + e1, x[1]);
-                }
-                float sum = 0.f;
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) sum = fmaf(x[0][e], x[0][e], fmaf(x[1][e], x[1][e], sum));
-                const float r = rsqrtf(row_sum<L>(sum) * (1.f / D) + a.eps);
-                float dot = 0.f;
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float dn0 = g[0][e] * c[e] + g[1][e] * s[e];
-                    const float dn1 = g[1][e] * c[e] - g[0][e] * s[e];
-                    x[0][e] *= r;
-                    x[1][e] *= r;
-                    dw[0][e] = fmaf(dn0, x[0][e], dw[0][e]);
-                    dw[1][e] = fmaf(dn1, x[1][e], dw[1][e]);
-                    g[0][e] = dn0 * w[0][e];
-                    g[1][e] = dn1 * w[1][e];
-                    dot = fmaf(g[0][e], x[0][e], fmaf(g[1][e], x[1][e], dot));
-                }
-                dot = row_sum<L>(dot) * (1.f / D);
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    g[0][e] = r * (g[0][e] - x[0][e] * dot);
-                    g[1][e] = r * (g[1][e] - x[1][e] * dot);
+            for (int h = 0; h < HP; ++h) {
+                g0[h] = g1[h] = Pr::fill(0.f);
+                x[h][0] = x[h][1] = make_uint4(0u, 0u, 0u, 0u);
+                if (pos >= 0 && h0 + hp + h < n_heads) {
+                    g0[h] = Pr::load_f32(dy + (hp + h) * dy_head + e0);
+                    g1[h] = Pr::load_f32(dy + (hp + h) * dy_head + e1);
+                    if (kind < 2) {
+                        x[h][0] = *reinterpret_cast<const uint4 *>(src + (hp + h) * D + e0);
+                        x[h][1] = *reinterpret_cast<const uint4 *>(src + (hp + h) * D + e1);
+                    }
                 }
             }
-            if (live && h0 + h < n_heads) {  // a padding row's gradient is zero
-                store_vec<T>(dst + (h0 + h) * D + e0, g[0]);
-                store_vec<T>(dst + (h0 + h) * D + e1, g[1]);
+#pragma unroll
+            for (int h = 0; h < HP; ++h) {
+                if (kind < 2) {
+                    Pr x0 = Pr::widen(x[h][0]), x1 = Pr::widen(x[h][1]);
+                    const Pr w0 = Pr::widen(wr[0]), w1 = Pr::widen(wr[1]);
+                    const float r = rms<T, D>(x0, x1, a.eps);
+                    float2 dot2 = both(0.f);
+#pragma unroll
+                    for (int j = 0; j < Pr::N; ++j) {
+                        const float2 dn0 = __ffma2_rn(g1[h].v[j], turn.s.v[j], __fmul2_rn(g0[h].v[j], turn.c.v[j]));
+                        const float2 dn1 = __ffma2_rn(g0[h].v[j], turn.ns.v[j], __fmul2_rn(g1[h].v[j], turn.c.v[j]));
+                        x0.v[j] = __fmul2_rn(x0.v[j], both(r));
+                        x1.v[j] = __fmul2_rn(x1.v[j], both(r));
+                        dw0.v[j] = __ffma2_rn(dn0, x0.v[j], dw0.v[j]);
+                        dw1.v[j] = __ffma2_rn(dn1, x1.v[j], dw1.v[j]);
+                        g0[h].v[j] = __fmul2_rn(dn0, w0.v[j]);
+                        g1[h].v[j] = __fmul2_rn(dn1, w1.v[j]);
+                        dot2 = __ffma2_rn(g0[h].v[j], x0.v[j], __ffma2_rn(g1[h].v[j], x1.v[j], dot2));
+                    }
+                    const float2 dot = both(-row_sum<L>(dot2.x + dot2.y) * (1.f / D));
+#pragma unroll
+                    for (int j = 0; j < Pr::N; ++j) {
+                        g0[h].v[j] = __fmul2_rn(__ffma2_rn(x0.v[j], dot, g0[h].v[j]), both(r));
+                        g1[h].v[j] = __fmul2_rn(__ffma2_rn(x1.v[j], dot, g1[h].v[j]), both(r));
+                    }
+                }
+                if (live && h0 + hp + h < n_heads) {  // a padding row's gradient is zero
+                    g0[h].store(dst + (hp + h) * D + e0);
+                    g1[h].store(dst + (hp + h) * D + e1);
+                }
             }
         }
     }
     if (kind == 2) return;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-        part[slot][e0 + e] = dw[0][e];
-        part[slot][e1 + e] = dw[1][e];
+    for (int j = 0; j < Pr::N; ++j) {
+        part[slot][e0 + 2 * j] = dw0.v[j].x;
+        part[slot][e0 + 2 * j + 1] = dw0.v[j].y;
+        part[slot][e1 + 2 * j] = dw1.v[j].x;
+        part[slot][e1 + 2 * j + 1] = dw1.v[j].y;
     }
     __syncthreads();
     for (int d = threadIdx.x; d < D; d += kThreads) {
@@ -279,20 +334,27 @@ __global__ void __launch_bounds__(kThreads) norm_rope_bwd_kernel(const NormRopeA
     }
 }
 
-// dw of q (blockIdx.y = 0) and k (1): the partials of its head groups, in order, in
-// 64 bits.  A CTA takes 8 dims with 32 threads each (every 32nd partial, then a tree).
+// dw of q (blockIdx.y = 0) and k (1): the partials of its head groups, in a fixed order, in
+// 64 bits.  A CTA takes 8 dims with 32 threads each.  Launched while the backward kernel
+// still runs; what it sums is there once the wait returns.
 template <int D>
 __global__ void __launch_bounds__(256) norm_rope_dw(const NormRopeArgs a, int grid_x) {
-    __shared__ double part[32][8];
+    __shared__ double part[8][8];
     const int kind = blockIdx.y, d = threadIdx.x % 8, slot = threadIdx.x / 8;
     const long long n = (long long)a.groups[kind] * grid_x;
     const float *p = a.partial + (kind ? (long long)a.groups[0] * grid_x * D : 0) + blockIdx.x * 8 + d;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     double sum = 0.0;
+#pragma unroll 8
     for (long long i = slot; i < n; i += 32) sum += (double)p[i * D];
-    part[slot][d] = sum;
+    sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+    if (threadIdx.x % 32 < 8) part[threadIdx.x / 32][d] = sum;
     __syncthreads();
-    if (slot == 0) {
-        for (int i = 1; i < 32; ++i) sum += part[i][d];
+    if (threadIdx.x < 8) {
+        sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += part[i][d];
         a.dw[kind][blockIdx.x * 8 + d] = (float)sum;
     }
 }
@@ -357,14 +419,14 @@ template <typename T, int D> hga_status_t launch_fwd(NormRopeArgs a, cudaStream_
     return record_cuda(cudaGetLastError());
 }
 
-// CTAs along the tokens of the backward: four CTAs per SM over all head groups.
-// A fixed number, so that the workspace size needs no device.
+// CTAs along the tokens of the backward: one wave of 148 SMs over all head groups.  A
+// fixed number, so that the workspace size needs no device.
 long long bwd_grid_x(const hga_proj_t &p) {
     const int lanes = p.head_dim / (p.dtype == HGA_FP32 ? 8 : 16);
     const int slots = kThreads / lanes;
     const long long steps = ((long long)p.batch * p.seq_len + slots - 1) / slots;
     const int groups = (p.n_q_heads + kHeads - 1) / kHeads + 2 * ((p.n_kv_heads + kHeads - 1) / kHeads);
-    const long long want = (148 * 4 + groups - 1) / groups;
+    const long long want = groups < 148 * kBwdCtas ? 148 * kBwdCtas / groups : 1;
     return steps < want ? steps : want;
 }
 
@@ -373,8 +435,16 @@ template <typename T, int D> hga_status_t launch_bwd(NormRopeArgs a, long long g
     norm_rope_bwd_kernel<T, D><<<dim3((unsigned)gx, a.groups[0] + 2 * a.groups[1]), kThreads, 0, stream>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return record_cuda(e);
-    norm_rope_dw<D><<<dim3(D / 8, 2), 256, 0, stream>>>(a, (int)gx);
-    return record_cuda(cudaGetLastError());
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(D / 8, 2);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return record_cuda(cudaLaunchKernelEx(&cfg, norm_rope_dw<D>, a, (int)gx));
 }
 
 }  // namespace
