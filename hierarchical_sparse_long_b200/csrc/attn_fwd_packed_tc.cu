@@ -18,9 +18,9 @@
 //   warps 1, 3  PV issuers: O_h += P_h V  (M128 N128 K64, P from TMEM)
 //   then 4 NH   softmax warps: one TMEM lane (= query row) per thread, online softmax in
 //               the log2 domain, P written back as bf16 pairs into the tile's S buffer
-//   last 4      producers.  History tiles: each thread holds a tile's worth of codes and
-//               grids in registers (40 words, loaded one tile ahead), widens them and
-//               stores 16 bytes per word into the K / V stage: K as [2 column halves]
+//   last 4      producers.  History tiles: records come as bulk copies into a ring of
+//               three in shared memory; a thread reads its share of the codes and grids,
+//               widens it and stores 16 bytes per word into the K / V stage: K as [2 column halves]
 //               [64 tokens][128 B], V transposed as [128 channels][128 B of tokens] --
 //               the record's own order, so one word is one swizzled 16-byte chunk in both
 //               -- hence V is K-major for these tiles.  Segment tiles: TMA, V as rows of
@@ -48,12 +48,14 @@ constexpr uint32_t IDESC_PV = tc::idesc_bf16(128, D, false, true);        // seg
 constexpr uint32_t IDESC_PV_HIST = tc::idesc_bf16(128, D, false, false);  // history: V rows are channels
 constexpr int kIssueWarps = 4;
 constexpr int kProdWarps = 4;
+constexpr int kRecStages = 3;  // records on their way to, or in, shared memory
 
 template <int NH> struct Smem {
     static constexpr uint32_t Q = 0;
     static constexpr uint32_t K = Q + NH * Q_HALF_BYTES;
     static constexpr uint32_t V = K + NSTAGE * KV_TILE_BYTES;
-    static constexpr uint32_t BAR = V + NSTAGE * KV_TILE_BYTES;
+    static constexpr uint32_t REC = V + NSTAGE * KV_TILE_BYTES;  // [kRecStages][record]
+    static constexpr uint32_t BAR = REC + kRecStages * Packed<D>::kRecord;
     static constexpr uint32_t TOTAL = BAR + 1024;
     static constexpr uint32_t ALLOC = TOTAL + 1024;  // + alignment slack
 };
@@ -75,6 +77,8 @@ struct Bars {
     uint64_t k_empty[NSTAGE];  // released once QK^T of the tile completes (both halves)
     uint64_t v_full[NSTAGE];
     uint64_t v_empty[NSTAGE];  // released once PV of the tile completes (both halves)
+    uint64_t r_full[kRecStages];   // a record in shared memory
+    uint64_t r_empty[kRecStages];  // and read by the producer warps
     uint64_t s_full[2][2];     // [half][S/P buffer]: S of the buffer's tile in TMEM
     uint64_t p_full[2][2];     // [half][S/P buffer]: P of the buffer's tile written to TMEM
     uint64_t o_done[2][2];     // [half][S/P buffer]: PV of the buffer's tile completed
@@ -137,9 +141,9 @@ struct KShare {
     uint32_t w[8], s[4], z[4];
     __device__ __forceinline__ void load(const uint8_t *rec, int o, int r0) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t *>(rec) + (r0 + 8 * i) * 16 + o);
-        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(rec + Packed<D>::kGridOff) + o);
-        const uint4 b = __ldg(reinterpret_cast<const uint4 *>(rec + Packed<D>::kGridOff + Packed<D>::kGridHalf) + o);
+        for (int i = 0; i < 8; ++i) w[i] = reinterpret_cast<const uint32_t *>(rec)[(r0 + 8 * i) * 16 + o];
+        const uint4 a = reinterpret_cast<const uint4 *>(rec + Packed<D>::kGridOff)[o];
+        const uint4 b = reinterpret_cast<const uint4 *>(rec + Packed<D>::kGridOff + Packed<D>::kGridHalf)[o];
         s[0] = a.x; s[1] = a.y; s[2] = a.z; s[3] = a.w;
         z[0] = b.x; z[1] = b.y; z[2] = b.z; z[3] = b.w;
     }
@@ -149,12 +153,12 @@ struct VShare {
     uint32_t w[8], s[2][4], z[2][4];
     __device__ __forceinline__ void load(const uint8_t *vrec, int o, int r0) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t *>(vrec) + (r0 + 16 * i) * 8 + o);
+        for (int i = 0; i < 8; ++i) w[i] = reinterpret_cast<const uint32_t *>(vrec)[(r0 + 16 * i) * 8 + o];
 #pragma unroll
         for (int gp = 0; gp < 2; ++gp) {
             const uint8_t *grid = vrec + Packed<D>::kGridOff + gp * 2 * TILE;
-            const uint4 a = __ldg(reinterpret_cast<const uint4 *>(grid) + o);
-            const uint4 b = __ldg(reinterpret_cast<const uint4 *>(grid + Packed<D>::kGridHalf) + o);
+            const uint4 a = reinterpret_cast<const uint4 *>(grid)[o];
+            const uint4 b = reinterpret_cast<const uint4 *>(grid + Packed<D>::kGridHalf)[o];
             s[gp][0] = a.x; s[gp][1] = a.y; s[gp][2] = a.z; s[gp][3] = a.w;
             z[gp][0] = b.x; z[gp][1] = b.y; z[gp][2] = b.z; z[gp][3] = b.w;
         }
@@ -190,6 +194,10 @@ __global__ void __launch_bounds__(32 * (kIssueWarps + 4 * NH + kProdWarps), 1)
             tc::mbar_init(&bars->v_full[s], kProdWarps);
             tc::mbar_init(&bars->v_empty[s], NH);
         }
+        for (int s = 0; s < kRecStages; ++s) {
+            tc::mbar_init(&bars->r_full[s], 1);
+            tc::mbar_init(&bars->r_empty[s], kProdWarps);
+        }
         for (int h = 0; h < 2; ++h)
             for (int bb = 0; bb < 2; ++bb) {
                 tc::mbar_init(&bars->s_full[h][bb], 1);
@@ -223,7 +231,8 @@ __global__ void __launch_bounds__(32 * (kIssueWarps + 4 * NH + kProdWarps), 1)
     volatile int *abort = &bars->abort;
     const int n_hist = bars->n_hist;          // history tiles, then segment tiles 0 .. m
     const int n_tiles = n_hist + m + 1;
-    int issued = 0;  // producer warp 0: tiles whose loads it has issued (drained on abort)
+    int issued = 0;   // producer warp 0: tiles whose loads it has issued, and
+    int records = 0;  // records asked for (drained on abort)
 
     if (warp < kIssueWarps) {
         // ------------------------------------------------------------ UMMA issuers
@@ -318,7 +327,17 @@ __global__ void __launch_bounds__(32 * (kIssueWarps + 4 * NH + kProdWarps), 1)
         const uint32_t kdst = sbase + L::K + (ko >> 3) * (64 * 128) + kr * 128 + (((ko & 7) ^ kr) << 4);
         const uint32_t vdst = sbase + L::V + vr * 128 + ((vo ^ (vr & 7)) << 4);
         const uint8_t *base = a.hist + (long long)bg * a.cap * Packed<D>::kRecord;
+        // the next record, as one bulk copy: ahead by kRecStages tiles, and without loads in
+        // flight in the threads, for which a proxy fence would wait
+        auto fetch = [&]() {
+            uint64_t *bar = &bars->r_full[records % kRecStages];
+            tc::mbar_arrive_expect_tx(bar, Packed<D>::kRecord);
+            tc::bulk_load(smem + L::REC + (records % kRecStages) * Packed<D>::kRecord,
+                          base + (long long)bars->tiles[records] * Packed<D>::kRecord, Packed<D>::kRecord, bar);
+            ++records;
+        };
         if (t == 0) {
+            while (records < n_hist && records < kRecStages) fetch();
             tc::tma_prefetch_desc(&tm_q);
             tc::tma_prefetch_desc(&tm_ks);
             tc::tma_prefetch_desc(&tm_vs);
@@ -343,19 +362,21 @@ __global__ void __launch_bounds__(32 * (kIssueWarps + 4 * NH + kProdWarps), 1)
             }
             __syncwarp();
         };
-        // A thread holds the codes and grids of one tile ahead.  They are asked for behind
-        // the tile's only proxy fence: a fence waits for the loads in flight before it, so
-        // one between K and V would wait for memory twice a tile.
-        KShare ks;
-        VShare vs;
-        auto load = [&](int j) {
-            const uint8_t *rec = base + (long long)bars->tiles[j] * Packed<D>::kRecord;
-            ks.load(rec, ko, kr);
-            vs.load(rec + Packed<D>::kPart, vo, vr);
-        };
-        if (n_hist > 0) load(0);
         for (int j = 0; j < n_tiles; ++j) {
             const int s = j % NSTAGE, u = j / NSTAGE;
+            // this thread's codes and grids of the tile, out of the record's stage
+            KShare ks;
+            VShare vs;
+            const int rs = j % kRecStages;
+            if (j < n_hist) {
+                if (!__all_sync(0xffffffffu, tc::mbar_wait(&bars->r_full[rs], (j / kRecStages) & 1, abort, a.status)))
+                    break;
+                const uint8_t *rec = smem + L::REC + rs * Packed<D>::kRecord;
+                ks.load(rec, ko, kr);
+                vs.load(rec + Packed<D>::kPart, vo, vr);
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bars->r_empty[rs]);
+            }
             // a stage frees once the products of the tile NSTAGE back have read it
             if (j >= NSTAGE &&
                 !__all_sync(0xffffffffu, tc::mbar_wait(&bars->k_empty[s], (u - 1) & 1, abort, a.status) &&
@@ -381,7 +402,13 @@ __global__ void __launch_bounds__(32 * (kIssueWarps + 4 * NH + kProdWarps), 1)
                     tc::mbar_arrive(&bars->k_full[s]);
                     tc::mbar_arrive(&bars->v_full[s]);
                 }
-                if (j + 1 < n_hist) load(j + 1);
+                bool ok = true;
+                if (t == 0 && records < n_hist) {
+                    // the stage of a record that every producer warp has read by now, or soon
+                    ok = tc::mbar_wait(&bars->r_empty[rs], (j / kRecStages) & 1, abort, a.status);
+                    if (ok) fetch();
+                }
+                if (!__all_sync(0xffffffffu, ok)) break;
             } else {
                 seg_tile(smem + L::K + s * KV_TILE_BYTES, &tm_ks, j, &bars->k_full[s]);
                 seg_tile(smem + L::V + s * KV_TILE_BYTES, &tm_vs, j, &bars->v_full[s]);
@@ -538,6 +565,8 @@ __global__ void __launch_bounds__(32 * (kIssueWarps + 4 * NH + kProdWarps), 1)
                 tc::mbar_wait(&bars->k_full[j % NSTAGE], (j / NSTAGE) & 1, &never, a.status, 1ll << 28);
                 tc::mbar_wait(&bars->v_full[j % NSTAGE], (j / NSTAGE) & 1, &never, a.status, 1ll << 28);
             }
+            for (int j = records < kRecStages ? 0 : records - kRecStages; j < records; ++j)
+                tc::mbar_wait(&bars->r_full[j % kRecStages], (j / kRecStages) & 1, &never, a.status, 1ll << 28);
             tc::mbar_wait(&bars->q_full, 0, &never, a.status, 1ll << 28);
         }
         if (warp < kIssueWarps && (warp >> 1) < NH) {
