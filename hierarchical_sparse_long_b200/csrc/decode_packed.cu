@@ -415,15 +415,27 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_packed_kernel(con
     tc::cluster_wait();
 }
 
-// CTAs per (batch, KV head): one wave of the device, at most a unit per warp.
+// CTAs per (batch, KV head): 1, 2, 4 or 8 (clusters of three took longer than their work
+// predicts), all resident at once.  With c CTAs on an SM a warp takes about 0.4 + 0.8 c us
+// per unit of D = 128 (1.16 alone, 1.87, 2.75 measured), and a cluster's merge about 0.5 us,
+// 1 us for eight CTAs; the least sum of both is taken.  Measured, us for 1 / 2 / 4 / 8 CTAs:
+//   8 pairs of 19 units    8.5 /  6.8 /  5.8 /  5.4      32 pairs of 20   9.0 /  7.1 /  6.2 /  7.0
+//   128 pairs of 36       15.2 / 14.2 / 20.2 / 27.1     192 pairs of 36  21.5 / 18.5 / 24.1 / 37.3
 int cluster_size(const hga_params_t &p, int n_local) {
-    const int units = (p.topk < p.n_hist_chunks ? p.topk : p.n_hist_chunks) + (n_local + kPiece - 1) / kPiece;
-    const long long bg = (long long)p.batch * p.n_kv_heads;
-    long long n = (long long)kCtasPerSm * sm_count() / bg;
-    const long long most = (units + kWarps - 1) / kWarps;
-    if (n > most) n = most;
-    if (n > kMaxCluster) n = kMaxCluster;
-    return n < 1 ? 1 : (int)n;
+    const long long units =
+        (p.topk < p.n_hist_chunks ? p.topk : p.n_hist_chunks) + ((long long)n_local + kPiece - 1) / kPiece;
+    const long long bg = (long long)p.batch * p.n_kv_heads, sms = sm_count();
+    int best = 1;
+    long long best_cost = 0;
+    for (int n = 1; n <= kMaxCluster && (n == 1 || bg * n <= kCtasPerSm * sms); n *= 2) {
+        const long long serial = (units + kWarps * n - 1) / (kWarps * n), on_sm = (bg * n + sms - 1) / sms;
+        const long long cost = serial * (4 + 8 * on_sm) + (n == 1 ? 0 : n == 8 ? 10 : 5);  // tenths of a us
+        if (n == 1 || cost < best_cost) {
+            best = n;
+            best_cost = cost;
+        }
+    }
+    return best;
 }
 
 template <int D> hga_status_t launch_d(const PackedDecodeArgs &a, unsigned bg, cudaStream_t stream) {
