@@ -98,7 +98,6 @@ struct FwdPackedArgs {
     int qb0, n_blocks;
     const uint8_t *hist;
     const int32_t *idx;
-    __nv_bfloat16 *out;
     float *lse;
     unsigned *status;
     float scale_log2;  // log2(e) / sqrt(D)
@@ -168,7 +167,8 @@ struct VShare {
 template <int NH>
 __global__ void __launch_bounds__(32 * (kIssueWarps + 4 * NH + kProdWarps), 1)
     attn_fwd_packed_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_ks,
-                           const __grid_constant__ CUtensorMap tm_vs, const FwdPackedArgs a) {
+                           const __grid_constant__ CUtensorMap tm_vs, const __grid_constant__ CUtensorMap tm_o,
+                           const FwdPackedArgs a) {
     using L = Smem<NH>;
     constexpr int kSoftmax0 = kIssueWarps, kProd0 = kIssueWarps + 4 * NH;
     extern __shared__ uint8_t smem_raw[];
@@ -529,8 +529,11 @@ __global__ void __launch_bounds__(32 * (kIssueWarps + 4 * NH + kProdWarps), 1)
             tc::fence_after_sync();
             const bool write = hh < a.hc;  // rows 64..127 repeat the head when HC = 1
             const long long row = ((long long)(b * a.n_q_heads + h0 + (write ? hh : 0))) * a.seg_len + m * TILE + i;
-            __nv_bfloat16 *orow = a.out + row * D;
             const float inv_l = 1.f / l_run;
+            // the rows go out through this half's Q tile, which its last product has read: a
+            // thread's 16-byte pieces in the swizzled layout, then two TMA stores per warp of
+            // 32 rows (76.0 -> 74.5 us on the 16K segment against stores from the registers)
+            uint8_t *stage = smem + L::Q + h * Q_HALF_BYTES;
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 32) {
                 uint32_t o[32];
@@ -538,15 +541,26 @@ __global__ void __launch_bounds__(32 * (kIssueWarps + 4 * NH + kProdWarps), 1)
                 tc::tmem_wait_ld();
 #pragma unroll
                 for (int c = 0; c < 32; c += 8) {
-                    if (!write) break;
-                    uint4 v;
-                    v.x = tc::pack_bf16(__uint_as_float(o[c + 0]) * inv_l, __uint_as_float(o[c + 1]) * inv_l);
-                    v.y = tc::pack_bf16(__uint_as_float(o[c + 2]) * inv_l, __uint_as_float(o[c + 3]) * inv_l);
-                    v.z = tc::pack_bf16(__uint_as_float(o[c + 4]) * inv_l, __uint_as_float(o[c + 5]) * inv_l);
-                    v.w = tc::pack_bf16(__uint_as_float(o[c + 6]) * inv_l, __uint_as_float(o[c + 7]) * inv_l);
-                    *reinterpret_cast<uint4 *>(orow + c0 + c) = v;
+                    uint32_t v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        v[e] = tc::pack_bf16(__uint_as_float(o[c + 2 * e]) * inv_l,
+                                             __uint_as_float(o[c + 2 * e + 1]) * inv_l);
+                    const uint32_t row = tc::smem_u32(stage) + (c0 >> 6) * (128 * 128) + r * 128;
+                    const int piece = (c0 & 63) / 8 + c / 8;
+                    tc::st_shared_v4(row + ((piece ^ (r & 7)) << 4), v[0], v[1], v[2], v[3]);
                 }
             }
+            tc::fence_proxy_async();
+            __syncwarp();
+            if (write && lane == 0) {
+                const int orow = (b * a.n_q_heads + h0 + hh) * a.seg_len + m * TILE + (i & 32);
+                tc::tma_store_2d(&tm_o, stage + quad * (32 * 128), 0, orow);
+                tc::tma_store_2d(&tm_o, stage + 128 * 128 + quad * (32 * 128), 64, orow);
+                tc::bulk_commit();
+                tc::bulk_wait_all();
+            }
+            __syncwarp();
             if (write) a.lse[row] = (m_run + __log2f(l_run)) * 0.69314718055994530942f;
         }
     }
@@ -590,10 +604,11 @@ template <int NH>
 hga_status_t launch_nh(const hga_params_t &p, const void *q, const uint8_t *hist, int cap, const void *ks,
                        const void *vs, const int32_t *idx, void *out, float *lse, unsigned *status,
                        cudaStream_t stream) {
-    CUtensorMap mq, mks, mvs;
+    CUtensorMap mq, mks, mvs, mo;
     const long long n_bg = (long long)p.batch * p.n_kv_heads;
     const unsigned long long seg_rows = (unsigned long long)((n_bg - 1) * p.seg_head_stride + p.seg_len);
-    if (!tma_rows_map(&mq, q, (unsigned long long)p.batch * p.n_q_heads * p.seg_len) ||
+    const unsigned long long q_rows = (unsigned long long)p.batch * p.n_q_heads * p.seg_len;
+    if (!tma_rows_map(&mq, q, q_rows) || !tma_rows_map(&mo, out, q_rows, 32) ||
         !tma_rows_map(&mks, ks, seg_rows) || !tma_rows_map(&mvs, vs, seg_rows)) {
         record_error("hga_attn_fwd_packed: TMA tensor map encoding failed");
         return HGA_ERR_UNSUPPORTED;
@@ -615,7 +630,6 @@ hga_status_t launch_nh(const hga_params_t &p, const void *q, const uint8_t *hist
     a.n_blocks = (p.qblock_end > 0 ? p.qblock_end : nqb) - a.qb0;
     a.hist = hist;
     a.idx = idx;
-    a.out = static_cast<__nv_bfloat16 *>(out);
     a.lse = lse;
     a.status = status;
     a.scale_log2 = (float)(1.4426950408889634 / __builtin_sqrt((double)D));
@@ -623,7 +637,7 @@ hga_status_t launch_nh(const hga_params_t &p, const void *q, const uint8_t *hist
     cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kern), (int)Smem<NH>::ALLOC);
     if (e != cudaSuccess) return record_cuda(e);
     const unsigned grid = (unsigned)(a.n_blocks * n_bg * a.n_sub);
-    kern<<<grid, 32 * (kIssueWarps + 4 * NH + kProdWarps), Smem<NH>::ALLOC, stream>>>(mq, mks, mvs, a);
+    kern<<<grid, 32 * (kIssueWarps + 4 * NH + kProdWarps), Smem<NH>::ALLOC, stream>>>(mq, mks, mvs, mo, a);
     return record_cuda(cudaGetLastError());
 }
 
