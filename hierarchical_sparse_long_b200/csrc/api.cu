@@ -885,8 +885,8 @@ hga_status_t hga_attn_fwd_packed(const hga_params_t *p, const void *q, const voi
     if (p->n_hist_chunks > 0 && !hist) return HGA_ERR_INVALID_ARG;
     for (const void *ptr : {q, hist, k_seg, v_seg, (const void *)out})
         if (ptr && !aligned16(ptr)) return HGA_ERR_INVALID_ARG;
-    if (!hga::attn_fwd_tc_shape(*p)) {
-        hga::record_error("hga_attn_fwd_packed runs on the tcgen05 kernel only (bf16, head_dim 128)");
+    if (!hga::attn_fwd_packed_shape(*p)) {
+        hga::record_error("hga_attn_fwd_packed takes bf16 only");
         return HGA_ERR_UNSUPPORTED;
     }
     if (!hga::attn_fwd_packed_supported(*p)) {

@@ -1,6 +1,6 @@
 // Exact-token attention forward over a packed history on the 5th-generation tensor cores
 // (tcgen05 / TMEM / TMA): bf16 queries and segment, 4-bit history (packed.cuh), fp32
-// accumulation, head_dim 128.
+// accumulation, head_dim 64 or 128.
 //
 // "Long-Context Fine-Tuning with Limited VRAM", technical summary section 2.1 (exact K/V
 // of the routed chunks attended with a local window): what attn_fwd_tc.cu computes, with
@@ -14,17 +14,18 @@
 //
 // Warp roles (NH = 2: 512 threads):
 //   warps 0, 2  QK issuers of halves 0, 1 (warp 0 also owns TMEM):
-//               S_h = Q_h K^T  (M128 N64 K128, K-major A and B, SW128)
-//   warps 1, 3  PV issuers: O_h += P_h V  (M128 N128 K64, P from TMEM)
+//               S_h = Q_h K^T  (M128 N64 KD, K-major A and B, SW128)
+//   warps 1, 3  PV issuers: O_h += P_h V  (M128 ND K64, P from TMEM)
 //   then 4 NH   softmax warps: one TMEM lane (= query row) per thread, online softmax in
 //               the log2 domain, P written back as bf16 pairs into the tile's S buffer
 //   last 4      producers.  History tiles: records come as bulk copies into a ring of
 //               three in shared memory; a thread reads its share of the codes and grids,
-//               widens it and stores 16 bytes per word into the K / V stage: K as [2 column halves]
-//               [64 tokens][128 B], V transposed as [128 channels][128 B of tokens] --
-//               the record's own order, so one word is one swizzled 16-byte chunk in both
-//               -- hence V is K-major for these tiles.  Segment tiles: TMA, V as rows of
-//               tokens (MN-major); the PV issuers pick descriptor and instruction by tile.
+//               widens it and stores 16 bytes per word into the K / V stage: K as
+//               [D / 64][64 tokens][128 B of channels], V transposed as [D channels][128 B
+//               of tokens] -- the record's own order, so one word is one swizzled 16-byte
+//               chunk in both -- hence V is K-major for these tiles.  Segment tiles: TMA, V
+//               as rows of tokens (MN-major); the PV issuers pick descriptor and instruction
+//               by tile.
 // A K (V) stage is full when all four producer warps have arrived; for a segment tile one
 // of them arrives with the byte count of its TMA boxes.
 // TMEM (512 columns): O_h at 128h, S_h double-buffered at 256 + 128h + 64b.
@@ -37,25 +38,21 @@ namespace hga {
 
 namespace {
 
-constexpr int D = 128;
 constexpr int TILE = 64;
 constexpr int NSTAGE = 4;
 constexpr float kRescaleLog2 = 8.f;  // lazy-rescale threshold on the running max (log2 units)
-constexpr uint32_t Q_HALF_BYTES = 128 * D * 2;   // [2 col halves][128 rows][128 B]
-constexpr uint32_t KV_TILE_BYTES = TILE * D * 2; // K [2 col halves][64 rows][128 B]; V also [128 rows][128 B]
-constexpr uint32_t IDESC_QK = tc::idesc_bf16(128, TILE, false, false);
-constexpr uint32_t IDESC_PV = tc::idesc_bf16(128, D, false, true);        // segment: V rows are tokens
-constexpr uint32_t IDESC_PV_HIST = tc::idesc_bf16(128, D, false, false);  // history: V rows are channels
 constexpr int kIssueWarps = 4;
 constexpr int kProdWarps = 4;
 constexpr int kRecStages = 3;  // records on their way to, or in, shared memory
 
-template <int NH> struct Smem {
+template <int D, int NH> struct Smem {
+    static constexpr uint32_t Q_HALF = 128 * D * 2;   // [D / 64][128 rows][128 B]
+    static constexpr uint32_t KV_TILE = TILE * D * 2;  // K [D / 64][64 rows][128 B]; V also [D rows][128 B]
     static constexpr uint32_t Q = 0;
-    static constexpr uint32_t K = Q + NH * Q_HALF_BYTES;
-    static constexpr uint32_t V = K + NSTAGE * KV_TILE_BYTES;
-    static constexpr uint32_t REC = V + NSTAGE * KV_TILE_BYTES;  // [kRecStages][record]
-    static constexpr uint32_t BAR = REC + kRecStages * Packed<D>::kRecord;
+    static constexpr uint32_t K = Q + NH * Q_HALF;
+    static constexpr uint32_t V = K + NSTAGE * KV_TILE;
+    static constexpr uint32_t REC = V + NSTAGE * KV_TILE;  // [kRecStages][record]
+    static constexpr uint32_t BAR = (REC + kRecStages * Packed<D>::kRecord + 1023) / 1024 * 1024;
     static constexpr uint32_t TOTAL = BAR + 1024;
     static constexpr uint32_t ALLOC = TOTAL + 1024;  // + alignment slack
 };
@@ -135,26 +132,28 @@ __device__ __forceinline__ void add2(float &d0, float &d1, float x0, float x1) {
         : "f"(x0), "f"(x1));
 }
 
-// Codes and grid of one thread's share of a K part: octet `o` of the tokens r0 + 8 i.
-struct KShare {
-    uint32_t w[8], s[4], z[4];
+// Codes and grid of one thread's share of a K part: octet `o` of every kStep-th token from r0.
+template <int D> struct KShare {
+    static constexpr int kOctets = D / 8, kStep = 32 * kProdWarps / kOctets, kWords = TILE / kStep;
+    uint32_t w[kWords], s[4], z[4];
     __device__ __forceinline__ void load(const uint8_t *rec, int o, int r0) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = reinterpret_cast<const uint32_t *>(rec)[(r0 + 8 * i) * 16 + o];
+        for (int i = 0; i < kWords; ++i) w[i] = reinterpret_cast<const uint32_t *>(rec)[(r0 + kStep * i) * kOctets + o];
         const uint4 a = reinterpret_cast<const uint4 *>(rec + Packed<D>::kGridOff)[o];
         const uint4 b = reinterpret_cast<const uint4 *>(rec + Packed<D>::kGridOff + Packed<D>::kGridHalf)[o];
         s[0] = a.x; s[1] = a.y; s[2] = a.z; s[3] = a.w;
         z[0] = b.x; z[1] = b.y; z[2] = b.z; z[3] = b.w;
     }
 };
-// The same of a V part: token octet `o` of the channels r0 + 16 i (i < 4: group 0).
-struct VShare {
-    uint32_t w[8], s[2][4], z[2][4];
+// The same of a V part: token octet `o` of every 16th channel from r0 (four to a group).
+template <int D> struct VShare {
+    static constexpr int kWords = D / 16;
+    uint32_t w[kWords], s[D / 64][4], z[D / 64][4];
     __device__ __forceinline__ void load(const uint8_t *vrec, int o, int r0) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = reinterpret_cast<const uint32_t *>(vrec)[(r0 + 16 * i) * 8 + o];
+        for (int i = 0; i < kWords; ++i) w[i] = reinterpret_cast<const uint32_t *>(vrec)[(r0 + 16 * i) * 8 + o];
 #pragma unroll
-        for (int gp = 0; gp < 2; ++gp) {
+        for (int gp = 0; gp < D / 64; ++gp) {
             const uint8_t *grid = vrec + Packed<D>::kGridOff + gp * 2 * TILE;
             const uint4 a = reinterpret_cast<const uint4 *>(grid)[o];
             const uint4 b = reinterpret_cast<const uint4 *>(grid + Packed<D>::kGridHalf)[o];
@@ -164,12 +163,15 @@ struct VShare {
     }
 };
 
-template <int NH>
+template <int D, int NH>
 __global__ void __launch_bounds__(32 * (kIssueWarps + 4 * NH + kProdWarps), 1)
     attn_fwd_packed_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_ks,
                            const __grid_constant__ CUtensorMap tm_vs, const __grid_constant__ CUtensorMap tm_o,
                            const FwdPackedArgs a) {
-    using L = Smem<NH>;
+    using L = Smem<D, NH>;
+    constexpr uint32_t IDESC_QK = tc::idesc_bf16(128, TILE, false, false);
+    constexpr uint32_t IDESC_PV = tc::idesc_bf16(128, D, false, true);        // segment: V rows are tokens
+    constexpr uint32_t IDESC_PV_HIST = tc::idesc_bf16(128, D, false, false);  // history: V rows are channels
     constexpr int kSoftmax0 = kIssueWarps, kProd0 = kIssueWarps + 4 * NH;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -244,7 +246,7 @@ __global__ void __launch_bounds__(32 * (kIssueWarps + 4 * NH + kProdWarps), 1)
             // to the start-address field (addresses stay below 2^18, so no carry).
             bool ok = true;
             if (qk) {
-                const uint64_t q_desc = tc::desc_sw128(sbase + L::Q + h * Q_HALF_BYTES, 16, 1024);
+                const uint64_t q_desc = tc::desc_sw128(sbase + L::Q + h * L::Q_HALF, 16, 1024);
                 const uint64_t k_desc = tc::desc_sw128(sbase + L::K, 16, 1024);
                 ok = __all_sync(0xffffffffu, tc::mbar_wait(&bars->q_full, 0, abort, a.status));
                 for (int j = 0; ok && j < n_tiles; ++j) {
@@ -260,7 +262,7 @@ __global__ void __launch_bounds__(32 * (kIssueWarps + 4 * NH + kProdWarps), 1)
                     if (h == 1 && j >= 1 && !__all_sync(0xffffffffu, wait_count(&bars->sm0_tiles, j, abort, a.status)))
                         break;
                     tc::fence_after_sync();
-                    const uint64_t kd = k_desc + (uint64_t)((s * KV_TILE_BYTES) >> 4);
+                    const uint64_t kd = k_desc + (uint64_t)((s * L::KV_TILE) >> 4);
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t koff = ((kk >> 2) * (64 * 128) + (kk & 3) * 32) >> 4;
@@ -291,7 +293,7 @@ __global__ void __launch_bounds__(32 * (kIssueWarps + 4 * NH + kProdWarps), 1)
                     // The instruction descriptors are constants: with a run-time one an issue
                     // takes twice as long.
                     const uint32_t pa = tmem + 256 + 128 * h + 64 * pb;
-                    const uint64_t voff = (uint64_t)((s * KV_TILE_BYTES) >> 4);
+                    const uint64_t voff = (uint64_t)((s * L::KV_TILE) >> 4);
                     if (t < n_hist) {
 #pragma unroll
                         for (int kk = 0; kk < TILE / 16; ++kk) {
@@ -320,11 +322,11 @@ __global__ void __launch_bounds__(32 * (kIssueWarps + 4 * NH + kProdWarps), 1)
     } else if (warp >= kProd0) {
         // ------------------------------------------------------------ producers
         const int t = (warp - kProd0) * 32 + lane;
-        const int ko = t & 15, kr = t >> 4;  // K: channel octet, first token
+        const int ko = t % KShare<D>::kOctets, kr = t / KShare<D>::kOctets;  // K: channel octet, first token
         const int vo = t & 7, vr = t >> 3;   // V: token octet, first channel
         // swizzle: a row's 16-byte chunk index is XORed with the row index mod 8, which
         // is the same for all rows of a thread
-        const uint32_t kdst = sbase + L::K + (ko >> 3) * (64 * 128) + kr * 128 + (((ko & 7) ^ kr) << 4);
+        const uint32_t kdst = sbase + L::K + (ko >> 3) * (64 * 128) + kr * 128 + (((ko & 7) ^ (kr & 7)) << 4);
         const uint32_t vdst = sbase + L::V + vr * 128 + ((vo ^ (vr & 7)) << 4);
         const uint8_t *base = a.hist + (long long)bg * a.cap * Packed<D>::kRecord;
         // the next record, as one bulk copy: ahead by kRecStages tiles, and without loads in
@@ -341,12 +343,12 @@ __global__ void __launch_bounds__(32 * (kIssueWarps + 4 * NH + kProdWarps), 1)
             tc::tma_prefetch_desc(&tm_q);
             tc::tma_prefetch_desc(&tm_ks);
             tc::tma_prefetch_desc(&tm_vs);
-            tc::mbar_arrive_expect_tx(&bars->q_full, NH * Q_HALF_BYTES);
+            tc::mbar_arrive_expect_tx(&bars->q_full, NH * L::Q_HALF);
             for (int hh = 0; hh < 2 * NH; ++hh) {
                 const int qrow = (b * a.n_q_heads + h0 + (a.hc == 1 ? 0 : hh)) * a.seg_len + m * TILE;
-                uint8_t *dst = smem + L::Q + (hh >> 1) * Q_HALF_BYTES + (hh & 1) * (64 * 128);
-                tc::tma_load_2d(dst, &tm_q, 0, qrow, &bars->q_full);
-                tc::tma_load_2d(dst + 128 * 128, &tm_q, 64, qrow, &bars->q_full);
+                uint8_t *dst = smem + L::Q + (hh >> 1) * L::Q_HALF + (hh & 1) * (64 * 128);
+                for (int c = 0; c < D / 64; ++c)
+                    tc::tma_load_2d(dst + c * (128 * 128), &tm_q, 64 * c, qrow, &bars->q_full);
             }
         }
         __syncwarp();
@@ -354,9 +356,8 @@ __global__ void __launch_bounds__(32 * (kIssueWarps + 4 * NH + kProdWarps), 1)
         auto seg_tile = [&](uint8_t *dst, const CUtensorMap *map, int j, uint64_t *bar) {
             if (t == 0) {
                 const int row = (int)((long long)bg * a.seg_stride + (long long)(j - n_hist) * TILE);
-                tc::mbar_arrive_expect_tx(bar, KV_TILE_BYTES);
-                tc::tma_load_2d(dst, map, 0, row, bar);
-                tc::tma_load_2d(dst + 64 * 128, map, 64, row, bar);
+                tc::mbar_arrive_expect_tx(bar, L::KV_TILE);
+                for (int c = 0; c < D / 64; ++c) tc::tma_load_2d(dst + c * (64 * 128), map, 64 * c, row, bar);
             } else if (lane == 0) {
                 tc::mbar_arrive(bar);
             }
@@ -365,8 +366,8 @@ __global__ void __launch_bounds__(32 * (kIssueWarps + 4 * NH + kProdWarps), 1)
         for (int j = 0; j < n_tiles; ++j) {
             const int s = j % NSTAGE, u = j / NSTAGE;
             // this thread's codes and grids of the tile, out of the record's stage
-            KShare ks;
-            VShare vs;
+            KShare<D> ks;
+            VShare<D> vs;
             const int rs = j % kRecStages;
             if (j < n_hist) {
                 if (!__all_sync(0xffffffffu, tc::mbar_wait(&bars->r_full[rs], (j / kRecStages) & 1, abort, a.status)))
@@ -384,16 +385,16 @@ __global__ void __launch_bounds__(32 * (kIssueWarps + 4 * NH + kProdWarps), 1)
                 break;
             if (j < n_hist) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < KShare<D>::kWords; ++i) {
                     uint32_t r[4];
                     packed_octet(ks.w[i], ks.s, ks.z, r);
-                    tc::st_shared_v4(kdst + s * KV_TILE_BYTES + i * 8 * 128, r[0], r[1], r[2], r[3]);
+                    tc::st_shared_v4(kdst + s * L::KV_TILE + i * KShare<D>::kStep * 128, r[0], r[1], r[2], r[3]);
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < VShare<D>::kWords; ++i) {
                     uint32_t r[4];
                     packed_octet(vs.w[i], vs.s[i >> 2], vs.z[i >> 2], r);
-                    tc::st_shared_v4(vdst + s * KV_TILE_BYTES + i * 16 * 128, r[0], r[1], r[2], r[3]);
+                    tc::st_shared_v4(vdst + s * L::KV_TILE + i * 16 * 128, r[0], r[1], r[2], r[3]);
                 }
                 // widened codes are visible to the tensor core before the warp arrives
                 tc::fence_proxy_async();
@@ -410,8 +411,8 @@ __global__ void __launch_bounds__(32 * (kIssueWarps + 4 * NH + kProdWarps), 1)
                 }
                 if (!__all_sync(0xffffffffu, ok)) break;
             } else {
-                seg_tile(smem + L::K + s * KV_TILE_BYTES, &tm_ks, j, &bars->k_full[s]);
-                seg_tile(smem + L::V + s * KV_TILE_BYTES, &tm_vs, j, &bars->v_full[s]);
+                seg_tile(smem + L::K + s * L::KV_TILE, &tm_ks, j, &bars->k_full[s]);
+                seg_tile(smem + L::V + s * L::KV_TILE, &tm_vs, j, &bars->v_full[s]);
             }
             issued = j + 1;
         }
@@ -533,7 +534,7 @@ __global__ void __launch_bounds__(32 * (kIssueWarps + 4 * NH + kProdWarps), 1)
             // the rows go out through this half's Q tile, which its last product has read: a
             // thread's 16-byte pieces in the swizzled layout, then two TMA stores per warp of
             // 32 rows (76.0 -> 74.5 us on the 16K segment against stores from the registers)
-            uint8_t *stage = smem + L::Q + h * Q_HALF_BYTES;
+            uint8_t *stage = smem + L::Q + h * L::Q_HALF;
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 32) {
                 uint32_t o[32];
@@ -555,8 +556,8 @@ __global__ void __launch_bounds__(32 * (kIssueWarps + 4 * NH + kProdWarps), 1)
             __syncwarp();
             if (write && lane == 0) {
                 const int orow = (b * a.n_q_heads + h0 + hh) * a.seg_len + m * TILE + (i & 32);
-                tc::tma_store_2d(&tm_o, stage + quad * (32 * 128), 0, orow);
-                tc::tma_store_2d(&tm_o, stage + 128 * 128 + quad * (32 * 128), 64, orow);
+                for (int c = 0; c < D / 64; ++c)
+                    tc::tma_store_2d(&tm_o, stage + c * (128 * 128) + quad * (32 * 128), 64 * c, orow);
                 tc::bulk_commit();
                 tc::bulk_wait_all();
             }
@@ -600,7 +601,7 @@ __global__ void __launch_bounds__(32 * (kIssueWarps + 4 * NH + kProdWarps), 1)
     }
 }
 
-template <int NH>
+template <int D, int NH>
 hga_status_t launch_nh(const hga_params_t &p, const void *q, const uint8_t *hist, int cap, const void *ks,
                        const void *vs, const int32_t *idx, void *out, float *lse, unsigned *status,
                        cudaStream_t stream) {
@@ -608,8 +609,8 @@ hga_status_t launch_nh(const hga_params_t &p, const void *q, const uint8_t *hist
     const long long n_bg = (long long)p.batch * p.n_kv_heads;
     const unsigned long long seg_rows = (unsigned long long)((n_bg - 1) * p.seg_head_stride + p.seg_len);
     const unsigned long long q_rows = (unsigned long long)p.batch * p.n_q_heads * p.seg_len;
-    if (!tma_rows_map(&mq, q, q_rows) || !tma_rows_map(&mo, out, q_rows, 32) ||
-        !tma_rows_map(&mks, ks, seg_rows) || !tma_rows_map(&mvs, vs, seg_rows)) {
+    if (!tma_rows_map(&mq, q, q_rows, 64, D) || !tma_rows_map(&mo, out, q_rows, 32, D) ||
+        !tma_rows_map(&mks, ks, seg_rows, 64, D) || !tma_rows_map(&mvs, vs, seg_rows, 64, D)) {
         record_error("hga_attn_fwd_packed: TMA tensor map encoding failed");
         return HGA_ERR_UNSUPPORTED;
     }
@@ -633,18 +634,22 @@ hga_status_t launch_nh(const hga_params_t &p, const void *q, const uint8_t *hist
     a.lse = lse;
     a.status = status;
     a.scale_log2 = (float)(1.4426950408889634 / __builtin_sqrt((double)D));
-    auto kern = attn_fwd_packed_kernel<NH>;
-    cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kern), (int)Smem<NH>::ALLOC);
+    auto kern = attn_fwd_packed_kernel<D, NH>;
+    cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(kern), (int)Smem<D, NH>::ALLOC);
     if (e != cudaSuccess) return record_cuda(e);
     const unsigned grid = (unsigned)(a.n_blocks * n_bg * a.n_sub);
-    kern<<<grid, 32 * (kIssueWarps + 4 * NH + kProdWarps), Smem<NH>::ALLOC, stream>>>(mq, mks, mvs, mo, a);
+    kern<<<grid, 32 * (kIssueWarps + 4 * NH + kProdWarps), Smem<D, NH>::ALLOC, stream>>>(mq, mks, mvs, mo, a);
     return record_cuda(cudaGetLastError());
 }
 
 }  // namespace
 
+bool attn_fwd_packed_shape(const hga_params_t &p) {
+    return p.dtype == HGA_BF16 && (p.head_dim == 64 || p.head_dim == 128) && p.chunk == 64 && p.q_block == 64;
+}
+
 bool attn_fwd_packed_supported(const hga_params_t &p) {
-    if (!attn_fwd_tc_shape(p)) return false;
+    if (!attn_fwd_packed_shape(p)) return false;
     // TMA row coordinates are 32-bit (queries and segment; the history is not read by TMA)
     if ((long long)p.batch * p.n_kv_heads * p.seg_head_stride >= (1ll << 31) ||
         (long long)p.batch * p.n_q_heads * p.seg_len >= (1ll << 31))
@@ -655,9 +660,10 @@ bool attn_fwd_packed_supported(const hga_params_t &p) {
 hga_status_t launch_attn_fwd_packed(const hga_params_t &p, const void *q, const uint8_t *hist, int cap,
                                     const void *ks, const void *vs, const int32_t *idx, void *out, float *lse,
                                     unsigned *status, cudaStream_t stream) {
-    if (p.n_q_heads / p.n_kv_heads % 4 == 0)
-        return launch_nh<2>(p, q, hist, cap, ks, vs, idx, out, lse, status, stream);
-    return launch_nh<1>(p, q, hist, cap, ks, vs, idx, out, lse, status, stream);
+    const bool two = p.n_q_heads / p.n_kv_heads % 4 == 0;  // halves of two heads
+    auto f = p.head_dim == 128 ? (two ? launch_nh<128, 2> : launch_nh<128, 1>)
+                               : (two ? launch_nh<64, 2> : launch_nh<64, 1>);
+    return f(p, q, hist, cap, ks, vs, idx, out, lse, status, stream);
 }
 
 }  // namespace hga

@@ -168,7 +168,9 @@ hga_status_t launch_pack_history(const void *k, const void *v, long long head_st
 hga_status_t launch_unpack_history(const uint8_t *hist, int cap, long long slices, int head_dim, int first_chunk,
                                    int n_chunks, hga_dtype_t dtype, void *k, void *v, long long head_stride,
                                    cudaStream_t stream);
-// attn_fwd_tc_shape, the TMA encoder is available and the segment's row coordinates fit 32 bits.
+// bf16, head_dim 64 or 128, 64-query blocks; and the TMA encoder is available and the
+// segment's row coordinates fit 32 bits.
+bool attn_fwd_packed_shape(const hga_params_t &p);
 bool attn_fwd_packed_supported(const hga_params_t &p);
 hga_status_t launch_attn_fwd_packed(const hga_params_t &p, const void *q, const uint8_t *hist, int cap,
                                     const void *ks, const void *vs, const int32_t *idx, void *out, float *lse,
@@ -185,7 +187,7 @@ bool tma_encoder_available();
 // 2-D TMA map over `rows` rows of 128 bf16 values (256 B), boxes of 64 values
 // x box_rows rows, 128-byte swizzle; maps are cached per thread by
 // (base, rows, box_rows).
-bool tma_rows_map(CUtensorMap *map, const void *base, unsigned long long rows, unsigned box_rows = 64);
+bool tma_rows_map(CUtensorMap *map, const void *base, unsigned long long rows, unsigned box_rows = 64, int D = 128);
 // 3-D TMA map over `groups` groups of `rows` rows of D (64 or 128) bf16 values,
 // group g starting group_stride_rows rows after group g - 1; boxes of 64 values
 // x 64 rows x 1 group, 128-byte swizzle; rows past `rows` read as zeros.

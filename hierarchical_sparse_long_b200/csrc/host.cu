@@ -20,6 +20,7 @@ struct MapEntry {
     const void *base;
     unsigned long long rows;
     unsigned box_rows;
+    int D;
     CUtensorMap map;
 };
 constexpr int kMapCache = 16;
@@ -51,15 +52,15 @@ bool tma_encoder_available() {
     return g_encode != nullptr;
 }
 
-bool tma_rows_map(CUtensorMap *map, const void *base, unsigned long long rows, unsigned box_rows) {
+bool tma_rows_map(CUtensorMap *map, const void *base, unsigned long long rows, unsigned box_rows, int D) {
     for (const MapEntry &e : t_maps)
-        if (e.base == base && e.rows == rows && e.box_rows == box_rows && base != nullptr) {
+        if (e.base == base && e.rows == rows && e.box_rows == box_rows && e.D == D && base != nullptr) {
             *map = e.map;
             return true;
         }
     if (!tma_encoder_available()) return false;
-    const cuuint64_t dims[2] = {128, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {128 * 2};
+    const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)D * 2};
     const cuuint32_t box[2] = {64, box_rows};
     const cuuint32_t estr[2] = {1, 1};
     if (g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
@@ -71,6 +72,7 @@ bool tma_rows_map(CUtensorMap *map, const void *base, unsigned long long rows, u
     slot.base = base;
     slot.rows = rows;
     slot.box_rows = box_rows;
+    slot.D = D;
     slot.map = *map;
     return true;
 }

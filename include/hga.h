@@ -658,8 +658,8 @@ hga_status_t hga_unpack_history(const void *hist, int hist_cap_chunks, int batch
 
 /* hga_attn_fwd over a packed history: history chunk j of head (b, g) is its record's
  * values; queries, segment and outputs as there.
- *   p: as for hga_attn_fwd (hist_head_stride is not used); bf16 with head_dim 128
- *     only, on the tcgen05 kernel (else HGA_ERR_UNSUPPORTED).
+ *   p: as for hga_attn_fwd (hist_head_stride is not used); bf16 (HGA_ERR_UNSUPPORTED
+ *     for fp32), any head_dim.
  *   hist: hist_cap_chunks >= n_hist_chunks records per (b, g); may be null when
  *     n_hist_chunks is 0.
  * The V rows of a block's own 64-token segment tile are all multiplied, those after

@@ -259,25 +259,30 @@ def test_decode(case):
     c.check()
 
 
-# (B, Hq, Hkv, topk, nc, blocks, routes)
+# (B, Hq, Hkv, D, topk, nc, blocks, routes)
 FWD = [
-    (1, 1, 1, 1, 0, 2, "random"),
-    (1, 4, 1, 1, 1, 2, "random"),
-    (1, 32, 8, 16, 24, 3, "random"),
-    (2, 8, 2, 8, 5, 2, "random"),
-    (1, 6, 2, 5, 9, 4, "holes"),     # three heads per KV head: one per CTA
-    (1, 4, 2, 3, 9, 5, "holes"),     # two
-    (2, 8, 1, 7, 12, 2, "random"),   # eight: two CTAs of four
-    (1, 4, 1, 64, 70, 2, "random"),
-    (1, 8, 2, 6, 9, 3, "none"),
-    (1, 4, 1, 6, 9, 2, "twice"),
+    (1, 1, 1, 128, 1, 0, 2, "random"),
+    (1, 4, 1, 128, 1, 1, 2, "random"),
+    (1, 32, 8, 128, 16, 24, 3, "random"),
+    (2, 8, 2, 128, 8, 5, 2, "random"),
+    (1, 6, 2, 128, 5, 9, 4, "holes"),     # three heads per KV head: one per CTA
+    (1, 4, 2, 128, 3, 9, 5, "holes"),     # two
+    (2, 8, 1, 128, 7, 12, 2, "random"),   # eight: two CTAs of four
+    (1, 4, 1, 128, 64, 70, 2, "random"),
+    (1, 8, 2, 128, 6, 9, 3, "none"),
+    (1, 4, 1, 128, 6, 9, 2, "twice"),
+    (1, 1, 1, 64, 1, 1, 1, "random"),
+    (2, 8, 2, 64, 9, 14, 3, "holes"),
+    (1, 6, 3, 64, 5, 9, 4, "random"),
+    (1, 5, 1, 64, 4, 3, 2, "random"),
+    (1, 16, 2, 64, 3, 0, 2, "random"),
 ]
 
 
 @pytest.mark.parametrize("case", FWD, ids=str)
 def test_forward(case):
-    B, Hq, Hkv, topk, nc, blocks, routes = case
-    c = Packed(B, Hq, Hkv, 128, topk, nc, 64 * blocks, blocks, routes=routes)
+    B, Hq, Hkv, D, topk, nc, blocks, routes = case
+    c = Packed(B, Hq, Hkv, D, topk, nc, 64 * blocks, blocks, routes=routes)
     c.run()
     c.check()
 

@@ -211,7 +211,8 @@ def test_packed_attention_refused(L, decode):
     for i in range(7):
         for b in [None] + ([ODD] if i in (0, 1, 2, 3, 5) else []):
             assert _attn(L, decode, ptrs=tuple(b if j == i else FAKE for j in range(7))) == INVALID, i
-    assert _attn(L, decode, **(dict(seg_len=64, q_block=64, seg_head_stride=64) if decode else dict(seg_len=1, q_block=1))) == UNSUPPORTED
+    other = dict(seg_len=64, q_block=64, seg_head_stride=64) if decode else dict(seg_len=1, q_block=1)
+    assert _attn(L, decode, **other) == UNSUPPORTED
 
 
 def test_packed_attention_refused_by_form(L):
@@ -220,7 +221,6 @@ def test_packed_attention_refused_by_form(L):
     assert _attn(L, True, n_q_heads=18) == UNSUPPORTED      # nine heads per KV head
     assert b"8 query heads" in L.hga_last_error()
     assert _attn(L, True, batch=1 << 15, n_kv_heads=1 << 13, n_q_heads=1 << 13) == UNSUPPORTED
-    assert _attn(L, False, head_dim=64) == UNSUPPORTED
     assert _attn(L, False, seg_len=100) == INVALID
     assert _attn(L, False, qblock_begin=1, qblock_end=3) == INVALID
     assert _attn(L, False, batch=1 << 14, seg_head_stride=1 << 20) == UNSUPPORTED  # rows beyond 32 bits
