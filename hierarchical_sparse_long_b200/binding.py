@@ -50,8 +50,25 @@ class CParams(ctypes.Structure):
                 ("qblock_end", ctypes.c_int), ("sink_chunks", ctypes.c_int)]
 
 
+class _Mirror:
+    """A dataclass whose C struct is built by the first call after a change of its fields."""
+
+    def __setattr__(self, name, value):
+        self.__dict__[name] = value
+        self.__dict__.pop("_ref", None)
+
+    def ref(self):
+        r = self.__dict__.get("_ref")
+        if r is None:
+            r = self.__dict__["_ref"] = ctypes.byref(self.c())
+        return r
+
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k != "_ref"}
+
+
 @dataclasses.dataclass
-class Params:
+class Params(_Mirror):
     """Mirror of ``hga_params_t`` (strides in tokens; 0/0 block range = all blocks)."""
     batch: int
     n_q_heads: int
@@ -86,7 +103,7 @@ class CProj(ctypes.Structure):
 
 
 @dataclasses.dataclass
-class ProjParams:
+class ProjParams(_Mirror):
     """Mirror of ``hga_proj_t`` (token strides in elements, -1: rows of one fused
     projection of (Hq + 2 Hkv) * D; kv_head_stride in tokens, -1: seq_len)."""
     batch: int
@@ -235,23 +252,20 @@ def hga_build_summaries(k, head_stride: int, batch: int, n_kv_heads: int, head_d
 
 def hga_route(p: Params, q, summ, summ_cap_chunks: int, idx, stream=None):
     """Top-k chunk routing per (batch, kv head, query block) into idx (int32)."""
-    cp = p.c()
-    _check(lib().hga_route(ctypes.byref(cp), _ptr(q), _ptr(summ), summ_cap_chunks, _ptr(idx), _stream(stream)),
+    _check(lib().hga_route(p.ref(), _ptr(q), _ptr(summ), summ_cap_chunks, _ptr(idx), _stream(stream)),
            "hga_route")
 
 
 def hga_route_causal(p: Params, q, summ, summ_cap_chunks: int, idx, stream=None):
     """Strictly causal routing: one route per token into idx [B][Hkv][S][k] (int32)."""
-    cp = p.c()
-    _check(lib().hga_route_causal(ctypes.byref(cp), _ptr(q), _ptr(summ), summ_cap_chunks, _ptr(idx),
+    _check(lib().hga_route_causal(p.ref(), _ptr(q), _ptr(summ), summ_cap_chunks, _ptr(idx),
                                   _stream(stream)), "hga_route_causal")
 
 
 def hga_route_groups(p: Params, q, gsumm, gsumm_cap_groups: int, idx, group: int, topg: int, gidx, stream=None):
     """Second routing stage: the topg best groups of `group` tokens inside each block's
     chosen chunks into gidx [B][Hkv][S/q_block][topg] (int32)."""
-    cp = p.c()
-    _check(lib().hga_route_groups(ctypes.byref(cp), _ptr(q), _ptr(gsumm), gsumm_cap_groups, _ptr(idx), group,
+    _check(lib().hga_route_groups(p.ref(), _ptr(q), _ptr(gsumm), gsumm_cap_groups, _ptr(idx), group,
                                   topg, _ptr(gidx), _stream(stream)), "hga_route_groups")
 
 
@@ -259,8 +273,7 @@ def hga_route_groups_tiered(p: Params, q, host_gsumm, gsumm_cap_groups: int, idx
                             stage_gsumm, stage_slots: int, scratch, idx_remapped, n_fetched=None, stream=None):
     """hga_route_groups from a device cache of group summaries whose misses are
     fetched from pinned host memory (p.hist_head_stride = gsumm_cap_groups * group)."""
-    cp = p.c()
-    _check(lib().hga_route_groups_tiered(ctypes.byref(cp), _ptr(q), _ptr(host_gsumm), gsumm_cap_groups, _ptr(idx),
+    _check(lib().hga_route_groups_tiered(p.ref(), _ptr(q), _ptr(host_gsumm), gsumm_cap_groups, _ptr(idx),
                                          group, topg, _ptr(gidx), _ptr(stage_gsumm), stage_slots, _ptr(scratch),
                                          _ptr(idx_remapped), _ptr(n_fetched), _stream(stream)),
            "hga_route_groups_tiered")
@@ -268,8 +281,7 @@ def hga_route_groups_tiered(p: Params, q, host_gsumm, gsumm_cap_groups: int, idx
 
 def hga_attn_fwd(p: Params, q, k_hist, v_hist, k_seg, v_seg, idx, out, lse, stream=None):
     """Exact-token attention forward over routed chunks + the causal segment."""
-    cp = p.c()
-    _check(lib().hga_attn_fwd(ctypes.byref(cp), _ptr(q), _ptr(k_hist), _ptr(v_hist), _ptr(k_seg), _ptr(v_seg),
+    _check(lib().hga_attn_fwd(p.ref(), _ptr(q), _ptr(k_hist), _ptr(v_hist), _ptr(k_seg), _ptr(v_seg),
                               _ptr(idx), _ptr(out), _ptr(lse), _stream(stream)), "hga_attn_fwd")
 
 
@@ -277,8 +289,7 @@ def hga_route_attn_fwd(p: Params, q, summ, summ_cap_chunks: int, idx, k_hist, v_
                        stream=None):
     """Route, then attend, in one call: the attention overlaps the route's tail
     (routes into idx as hga_route; out/lse as hga_attn_fwd within rounding)."""
-    cp = p.c()
-    _check(lib().hga_route_attn_fwd(ctypes.byref(cp), _ptr(q), _ptr(summ), summ_cap_chunks, _ptr(idx),
+    _check(lib().hga_route_attn_fwd(p.ref(), _ptr(q), _ptr(summ), summ_cap_chunks, _ptr(idx),
                                     _ptr(k_hist), _ptr(v_hist), _ptr(k_seg), _ptr(v_seg), _ptr(out), _ptr(lse),
                                     _stream(stream)), "hga_route_attn_fwd")
 
@@ -286,8 +297,7 @@ def hga_route_attn_fwd(p: Params, q, summ, summ_cap_chunks: int, idx, k_hist, v_
 def hga_attn_fwd_groups(p: Params, q, k_hist, v_hist, k_seg, v_seg, gidx, group: int, topg: int, out, lse,
                         stream=None):
     """Attention over the routed groups (hga_route_groups) + the causal segment."""
-    cp = p.c()
-    _check(lib().hga_attn_fwd_groups(ctypes.byref(cp), _ptr(q), _ptr(k_hist), _ptr(v_hist), _ptr(k_seg),
+    _check(lib().hga_attn_fwd_groups(p.ref(), _ptr(q), _ptr(k_hist), _ptr(v_hist), _ptr(k_seg),
                                      _ptr(v_seg), _ptr(gidx), group, topg, _ptr(out), _ptr(lse), _stream(stream)),
            "hga_attn_fwd_groups")
 
@@ -295,24 +305,21 @@ def hga_attn_fwd_groups(p: Params, q, k_hist, v_hist, k_seg, v_seg, gidx, group:
 def hga_attn_bwd_groups(p: Params, q, k_hist, v_hist, k_seg, v_seg, gidx, group: int, topg: int, out, lse, dout,
                         dq, dk_seg, dv_seg, workspace, stream=None):
     """Backward of hga_attn_fwd_groups: dq over routed groups and segment, dk/dv of the segment."""
-    cp = p.c()
     nbytes = workspace.numel() * workspace.element_size()
-    _check(lib().hga_attn_bwd_groups(ctypes.byref(cp), _ptr(q), _ptr(k_hist), _ptr(v_hist), _ptr(k_seg),
+    _check(lib().hga_attn_bwd_groups(p.ref(), _ptr(q), _ptr(k_hist), _ptr(v_hist), _ptr(k_seg),
                                      _ptr(v_seg), _ptr(gidx), group, topg, _ptr(out), _ptr(lse), _ptr(dout), _ptr(dq),
                                      _ptr(dk_seg), _ptr(dv_seg), _ptr(workspace), nbytes, _stream(stream)),
            "hga_attn_bwd_groups")
 
 
 def hga_attn_causal_workspace_size(p: Params, backward: bool = False) -> int:
-    cp = p.c()
-    return int(lib().hga_attn_causal_workspace_size(ctypes.byref(cp), 1 if backward else 0))
+    return int(lib().hga_attn_causal_workspace_size(p.ref(), 1 if backward else 0))
 
 
 def hga_attn_fwd_causal(p: Params, q, k_hist, v_hist, k_seg, v_seg, idx_tok, out, lse, workspace, stream=None):
     """Attention over per-token (strictly causal) routes [B][Hkv][S][k] + the causal segment."""
-    cp = p.c()
     nbytes = workspace.numel() * workspace.element_size()
-    _check(lib().hga_attn_fwd_causal(ctypes.byref(cp), _ptr(q), _ptr(k_hist), _ptr(v_hist), _ptr(k_seg),
+    _check(lib().hga_attn_fwd_causal(p.ref(), _ptr(q), _ptr(k_hist), _ptr(v_hist), _ptr(k_seg),
                                      _ptr(v_seg), _ptr(idx_tok), _ptr(out), _ptr(lse), _ptr(workspace), nbytes,
                                      _stream(stream)), "hga_attn_fwd_causal")
 
@@ -320,40 +327,35 @@ def hga_attn_fwd_causal(p: Params, q, k_hist, v_hist, k_seg, v_seg, idx_tok, out
 def hga_attn_bwd_causal(p: Params, q, k_hist, v_hist, k_seg, v_seg, idx_tok, out, lse, dout, dq, dk_seg, dv_seg,
                         workspace, stream=None):
     """Backward of hga_attn_fwd_causal."""
-    cp = p.c()
     nbytes = workspace.numel() * workspace.element_size()
-    _check(lib().hga_attn_bwd_causal(ctypes.byref(cp), _ptr(q), _ptr(k_hist), _ptr(v_hist), _ptr(k_seg),
+    _check(lib().hga_attn_bwd_causal(p.ref(), _ptr(q), _ptr(k_hist), _ptr(v_hist), _ptr(k_seg),
                                      _ptr(v_seg), _ptr(idx_tok), _ptr(out), _ptr(lse), _ptr(dout), _ptr(dq),
                                      _ptr(dk_seg), _ptr(dv_seg), _ptr(workspace), nbytes, _stream(stream)),
            "hga_attn_bwd_causal")
 
 
 def hga_attn_decode_workspace_size(p: Params, n_local: int) -> int:
-    cp = p.c()
-    return int(lib().hga_attn_decode_workspace_size(ctypes.byref(cp), n_local))
+    return int(lib().hga_attn_decode_workspace_size(p.ref(), n_local))
 
 
 def hga_attn_decode(p: Params, q, k_hist, v_hist, k_local, v_local, n_local: int, idx, out, lse, workspace,
                     stream=None):
     """One new token per sequence: attention over its routed chunks and its n_local-token local window."""
-    cp = p.c()
     nbytes = workspace.numel() * workspace.element_size()
-    _check(lib().hga_attn_decode(ctypes.byref(cp), _ptr(q), _ptr(k_hist), _ptr(v_hist), _ptr(k_local),
+    _check(lib().hga_attn_decode(p.ref(), _ptr(q), _ptr(k_hist), _ptr(v_hist), _ptr(k_local),
                                  _ptr(v_local), n_local, _ptr(idx), _ptr(out), _ptr(lse), _ptr(workspace), nbytes,
                                  _stream(stream)), "hga_attn_decode")
 
 
 def hga_attn_bwd_workspace_size(p: Params) -> int:
-    cp = p.c()
-    return int(lib().hga_attn_bwd_workspace_size(ctypes.byref(cp)))
+    return int(lib().hga_attn_bwd_workspace_size(p.ref()))
 
 
 def hga_attn_bwd(p: Params, q, k_hist, v_hist, k_seg, v_seg, idx, out, lse, dout, dq, dk_seg, dv_seg,
                  workspace, stream=None):
     """Backward with frozen routes: dq (history + segment keys), dk/dv of the segment only."""
-    cp = p.c()
     nbytes = workspace.numel() * workspace.element_size()
-    _check(lib().hga_attn_bwd(ctypes.byref(cp), _ptr(q), _ptr(k_hist), _ptr(v_hist), _ptr(k_seg), _ptr(v_seg),
+    _check(lib().hga_attn_bwd(p.ref(), _ptr(q), _ptr(k_hist), _ptr(v_hist), _ptr(k_seg), _ptr(v_seg),
                               _ptr(idx), _ptr(out), _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dk_seg), _ptr(dv_seg),
                               _ptr(workspace), nbytes, _stream(stream)), "hga_attn_bwd")
 
@@ -364,31 +366,27 @@ def hga_attn_bwd_noalloc(p: Params, q, k_hist, v_hist, k_seg, v_seg, idx, out, l
     workspace is a fixed array inside the library (batch * q heads * segment
     length <= 1,048,576).  Calls on one device share that array, so calls
     that overlap on the GPU must be serialised by the caller."""
-    cp = p.c()
-    _check(lib().hga_attn_bwd_noalloc(ctypes.byref(cp), _ptr(q), _ptr(k_hist), _ptr(v_hist), _ptr(k_seg),
+    _check(lib().hga_attn_bwd_noalloc(p.ref(), _ptr(q), _ptr(k_hist), _ptr(v_hist), _ptr(k_seg),
                                       _ptr(v_seg), _ptr(idx), _ptr(out), _ptr(lse), _ptr(dout), _ptr(dq),
                                       _ptr(dk_seg), _ptr(dv_seg), _stream(stream)), "hga_attn_bwd_noalloc")
 
 
 def hga_tier_scratch_size(p: Params, stage_slots: int) -> int:
     """Bytes of int32 scratch the tiered staging cache of stage_slots tiles needs."""
-    cp = p.c()
-    return int(lib().hga_tier_scratch_size(ctypes.byref(cp), stage_slots))
+    return int(lib().hga_tier_scratch_size(p.ref(), stage_slots))
 
 
 def hga_tier_reset(p: Params, stage_slots: int, scratch, stream=None):
     """Marks every slot of the staging cache empty."""
-    cp = p.c()
-    _check(lib().hga_tier_reset(ctypes.byref(cp), stage_slots, _ptr(scratch), _stream(stream)), "hga_tier_reset")
+    _check(lib().hga_tier_reset(p.ref(), stage_slots, _ptr(scratch), _stream(stream)), "hga_tier_reset")
 
 
 def hga_fetch_tiered(p: Params, host_k, host_v, idx, qblock_begin: int, qblock_end: int, stage_k, stage_v,
                      stage_slots: int, scratch, idx_remapped, n_fetched=None, copy_stream=None, done=None):
     """One fetch wave: the routed tiles of blocks [qblock_begin, qblock_end) the staging
     cache does not hold are copied from pinned host memory; idx_remapped gets slots."""
-    cp = p.c()
     ev = None if done is None else ctypes.c_void_p(done.cuda_event)
-    _check(lib().hga_fetch_tiered(ctypes.byref(cp), _ptr(host_k), _ptr(host_v), _ptr(idx), qblock_begin,
+    _check(lib().hga_fetch_tiered(p.ref(), _ptr(host_k), _ptr(host_v), _ptr(idx), qblock_begin,
                                   qblock_end, _ptr(stage_k), _ptr(stage_v), stage_slots, _ptr(scratch),
                                   _ptr(idx_remapped), _ptr(n_fetched), _stream(copy_stream), ev),
            "hga_fetch_tiered")
@@ -396,8 +394,7 @@ def hga_fetch_tiered(p: Params, host_k, host_v, idx, qblock_begin: int, qblock_e
 
 def hga_tier_offload(p: Params, k_seg, v_seg, host_k, host_v, dst_token: int, stream=None):
     """Copies the segment's K/V (every (b, g) slice) into the pinned host history at dst_token."""
-    cp = p.c()
-    _check(lib().hga_tier_offload(ctypes.byref(cp), _ptr(k_seg), _ptr(v_seg), _ptr(host_k), _ptr(host_v),
+    _check(lib().hga_tier_offload(p.ref(), _ptr(k_seg), _ptr(v_seg), _ptr(host_k), _ptr(host_v),
                                   dst_token, _stream(stream)), "hga_tier_offload")
 
 
@@ -453,9 +450,8 @@ def hga_attn_fwd_tiered(p: Params, q, host_k, host_v, k_seg, v_seg, idx, out, ls
     """Attention over host-resident history: fetch waves on copy_stream overlapped with
     earlier waves' attention on stream, ordered by sched (a TierSched); the previous
     segment's chunks are copied from prev_k_seg / prev_v_seg when given."""
-    cp = p.c()
     flags = (HGA_TIER_RESET if reset_cache else 0) | (HGA_TIER_CHAIN if chain else 0)
-    _check(lib().hga_attn_fwd_tiered(ctypes.byref(cp), _ptr(q), _ptr(host_k), _ptr(host_v), _ptr(k_seg),
+    _check(lib().hga_attn_fwd_tiered(p.ref(), _ptr(q), _ptr(host_k), _ptr(host_v), _ptr(k_seg),
                                      _ptr(v_seg), _ptr(prev_k_seg), _ptr(prev_v_seg), _ptr(idx), _ptr(out),
                                      _ptr(lse), _ptr(stage_k), _ptr(stage_v),
                                      stage_slots, _ptr(scratch), _ptr(idx_remapped), wave_blocks, flags,
@@ -468,8 +464,7 @@ def hga_segment_fwd(p: Params, q, k_hist, v_hist, k_seg, v_seg, summ, summ_cap_c
     """One segment of an evaluation over resident history: route and summary append on
     route_stream, attention on stream (a segment's route runs under the previous
     segment's attention)."""
-    cp = p.c()
-    _check(lib().hga_segment_fwd(ctypes.byref(cp), _ptr(q), _ptr(k_hist), _ptr(v_hist), _ptr(k_seg), _ptr(v_seg),
+    _check(lib().hga_segment_fwd(p.ref(), _ptr(q), _ptr(k_hist), _ptr(v_hist), _ptr(k_seg), _ptr(v_seg),
                                  _ptr(summ), summ_cap_chunks, _ptr(idx), _ptr(out), _ptr(lse),
                                  HGA_TIER_RESET if reset else 0, _stream(stream), _stream(route_stream),
                                  ctypes.byref(sched.c)), "hga_segment_fwd")
@@ -482,8 +477,7 @@ def hga_segment_fwd_tiered(p: Params, q, k_seg, v_seg, summ, summ_cap_chunks: in
     """One segment of a tiered evaluation: route and summary append on route_stream,
     fetches on copy_stream (the previous segment's chunks from prev_k_seg / prev_v_seg
     when given), the K/V offload on offload_stream, attention on stream."""
-    cp = p.c()
-    _check(lib().hga_segment_fwd_tiered(ctypes.byref(cp), _ptr(q), _ptr(k_seg), _ptr(v_seg), _ptr(prev_k_seg),
+    _check(lib().hga_segment_fwd_tiered(p.ref(), _ptr(q), _ptr(k_seg), _ptr(v_seg), _ptr(prev_k_seg),
                                         _ptr(prev_v_seg), _ptr(summ),
                                         summ_cap_chunks, _ptr(idx), _ptr(host_k), _ptr(host_v), _ptr(out), _ptr(lse),
                                         _ptr(stage_k), _ptr(stage_v), stage_slots, _ptr(scratch),
@@ -511,24 +505,21 @@ def _table_rows(p: ProjParams, table) -> int:
 def hga_qk_norm_rope(p: ProjParams, q, k, v, q_weight, k_weight, table, positions, q_out, k_out, v_out, stream=None):
     """Per-head norm of q and k, position rotation and head-major layout of q, k and v from a
     layer's projections; positions int32 [B][S] (-1: padding row) or None for p.first_pos + i."""
-    cp = p.c()
-    _check(lib().hga_qk_norm_rope(ctypes.byref(cp), _ptr(q), _ptr(k), _ptr(v), _ptr(q_weight), _ptr(k_weight),
+    _check(lib().hga_qk_norm_rope(p.ref(), _ptr(q), _ptr(k), _ptr(v), _ptr(q_weight), _ptr(k_weight),
                                   _ptr(table), _table_rows(p, table), _ptr(positions), _ptr(q_out), _ptr(k_out),
                                   _ptr(v_out), _stream(stream)), "hga_qk_norm_rope")
 
 
 def hga_qk_norm_rope_workspace_size(p: ProjParams) -> int:
-    cp = p.c()
-    return int(lib().hga_qk_norm_rope_workspace_size(ctypes.byref(cp)))
+    return int(lib().hga_qk_norm_rope_workspace_size(p.ref()))
 
 
 def hga_qk_norm_rope_bwd(p: ProjParams, q, k, q_weight, k_weight, table, positions, dq, dk, dv, dq_in, dk_in, dv_in,
                          dq_weight, dk_weight, workspace, stream=None):
     """Backward of hga_qk_norm_rope: gradients of the projections (dtype) and of the weights (fp32)
     from the attention's fp32 dq, dk, dv."""
-    cp = p.c()
     nbytes = workspace.numel() * workspace.element_size()
-    _check(lib().hga_qk_norm_rope_bwd(ctypes.byref(cp), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight),
+    _check(lib().hga_qk_norm_rope_bwd(p.ref(), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight),
                                       _ptr(table), _table_rows(p, table), _ptr(positions), _ptr(dq), _ptr(dk),
                                       _ptr(dv), _ptr(dq_in), _ptr(dk_in), _ptr(dv_in), _ptr(dq_weight),
                                       _ptr(dk_weight), _ptr(workspace), nbytes, _stream(stream)),
@@ -559,8 +550,7 @@ def hga_unpack_history(hist, hist_cap_chunks: int, batch: int, n_kv_heads: int, 
 
 def hga_attn_fwd_packed(p: Params, q, hist, hist_cap_chunks: int, k_seg, v_seg, idx, out, lse, stream=None):
     """hga_attn_fwd over a packed (4-bit) history."""
-    cp = p.c()
-    _check(lib().hga_attn_fwd_packed(ctypes.byref(cp), _ptr(q), _ptr(hist), hist_cap_chunks, _ptr(k_seg),
+    _check(lib().hga_attn_fwd_packed(p.ref(), _ptr(q), _ptr(hist), hist_cap_chunks, _ptr(k_seg),
                                      _ptr(v_seg), _ptr(idx), _ptr(out), _ptr(lse), _stream(stream)),
            "hga_attn_fwd_packed")
 
@@ -568,8 +558,7 @@ def hga_attn_fwd_packed(p: Params, q, hist, hist_cap_chunks: int, k_seg, v_seg, 
 def hga_attn_decode_packed(p: Params, q, hist, hist_cap_chunks: int, k_local, v_local, n_local: int, idx, out, lse,
                            stream=None):
     """hga_attn_decode over a packed (4-bit) history; the local window is bf16."""
-    cp = p.c()
-    _check(lib().hga_attn_decode_packed(ctypes.byref(cp), _ptr(q), _ptr(hist), hist_cap_chunks, _ptr(k_local),
+    _check(lib().hga_attn_decode_packed(p.ref(), _ptr(q), _ptr(hist), hist_cap_chunks, _ptr(k_local),
                                         _ptr(v_local), n_local, _ptr(idx), _ptr(out), _ptr(lse), _stream(stream)),
            "hga_attn_decode_packed")
 

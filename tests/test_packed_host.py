@@ -231,3 +231,24 @@ def test_binding_raises():
     t = torch.empty(4096, dtype=torch.uint8)
     with pytest.raises(hga.HGAError):
         hga.hga_attn_decode_packed(hga.Params(**{**ATTN, "seg_len": 1, "q_block": 1}), t, t, 7, t, t, 1, t, t, t, stream=0)
+
+
+def test_params_struct_follows_the_fields():
+    """The C struct of a Params is kept between calls and made anew after a change."""
+    import copy
+    import dataclasses
+    import pickle
+    p = hga.Params(**ATTN)
+    struct = lambda q: q.ref()._obj
+    assert p.ref() is p.ref() and struct(p).topk == 4 and struct(p).hist_head_stride == 8 * 64
+    other, again = copy.copy(p), pickle.loads(pickle.dumps(p))
+    p.topk, p.n_hist_chunks = 7, 9
+    assert struct(p).topk == 7 and struct(p).hist_head_stride == 9 * 64
+    for q in (other, again, copy.deepcopy(other), dataclasses.replace(other)):
+        assert q == hga.Params(**ATTN) and struct(q).topk == 4
+    setattr(other, "qblock_end", 2)
+    assert struct(other).qblock_end == 2
+    q = _proj()
+    assert struct(q).seq_len == 5
+    q.seq_len = 6
+    assert struct(q).seq_len == 6 and struct(q).kv_head_stride == 6
