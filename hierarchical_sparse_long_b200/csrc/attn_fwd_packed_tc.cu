@@ -68,6 +68,16 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
         : "memory");
 }
 
+// 2D tiled store of shared memory (visible to the async proxy) to (x, y), in this thread's
+// bulk group; the wait returns once the group's stores are done.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void *src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
+                 ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(tc::smem_u32(src))
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 struct Bars {
     uint64_t q_full;
     uint64_t k_full[NSTAGE];
@@ -560,9 +570,9 @@ __global__ void __launch_bounds__(32 * (kIssueWarps + 4 * NH + kProdWarps), 1)
             if (write && lane == 0) {
                 const int orow = (b * a.n_q_heads + h0 + hh) * a.seg_len + m * TILE + (i & 32);
                 for (int c = 0; c < D / 64; ++c)
-                    tc::tma_store_2d(&tm_o, stage + c * (128 * 128) + quad * (32 * 128), 64 * c, orow);
-                tc::bulk_commit();
-                tc::bulk_wait_all();
+                    tma_store_2d(&tm_o, stage + c * (128 * 128) + quad * (32 * 128), 64 * c, orow);
+                bulk_commit();
+                bulk_wait_all();
             }
             __syncwarp();
             if (write) a.lse[row] = (m_run + __log2f(l_run)) * 0.69314718055994530942f;
