@@ -13,12 +13,15 @@
 // (the extremes propagate NaN, an infinity makes s infinite) or s or z is not: the
 // group's values read as NaN.
 //
-// pack is bound by HBM: K and V are read once (the summaries come from the same read),
-// and 0.28 of their bytes written.  One 256-thread CTA takes a chunk, all of its loads in
+// pack's floor is HBM: K and V are read once (the summaries come from the same read), and
+// 0.28 of their bytes written.  One 256-thread CTA takes a chunk, all of its loads in
 // flight; K's extremes and sums cross threads through shared memory, V's stay in the lanes
 // of a row, and V's codes are turned there from token to channel order.  Choosing 16,384
-// codes a chunk costs about as much issue time as its bytes cost bandwidth, so the choice
-// is made of two-element FMAs and one multiply-add into the word.
+// codes a chunk costs more issue time (0.61 of the slots) than its bytes cost bandwidth, so
+// the choice is made of two-element FMAs and one multiply-add into the word: 22.6 us for
+// 1,792 bf16 chunks of D = 128 (75 MB: 11.5 us at the measured copy rate) against 56 us with
+// a rounding, a conversion and a 64-bit decision of the border cases per element; K and V in
+// CTAs of their own, at twice the CTAs, took 10 us more.
 #include <cfloat>
 
 #include "packed.cuh"
@@ -135,7 +138,8 @@ __device__ __noinline__ uint32_t exact_nibbles(uint4 x, const uint32_t *grids, u
 #pragma unroll
     for (int e = 0; e < N; ++e) {
         const int sh = code_shift<true>(e);
-        const float f = __uint_as_float(N == 4 ? raw[e % 4] : (e & 1 ? raw[e / 2 % 4] & 0xFFFF0000u : raw[e / 2 % 4] << 16));
+        const uint32_t bf = raw[e / 2 % 4];  // bf16: the word that holds element e
+        const float f = __uint_as_float(N == 4 ? raw[e % 4] : (e & 1 ? bf & 0xFFFF0000u : bf << 16));
         w |= exact_code(f, grid_of(grids[e]), word >> sh & 15u) << sh;
     }
     return w;
@@ -153,7 +157,8 @@ template <> struct Ext<__nv_bfloat16> {
     }
     __device__ __forceinline__ static Ext row(const uint4 &u) {  // of 8 elements
         const uint32_t hi = max2(max2(u.x, u.y), max2(u.z, u.w));
-        const uint32_t lo = max2(max2(u.x ^ 0x80008000u, u.y ^ 0x80008000u), max2(u.z ^ 0x80008000u, u.w ^ 0x80008000u));
+        constexpr uint32_t sign = 0x80008000u;
+        const uint32_t lo = max2(max2(u.x ^ sign, u.y ^ sign), max2(u.z ^ sign, u.w ^ sign));
         return {max2(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632))};
     }
     __device__ __forceinline__ Ext with(Ext o) const { return {max2(w, o.w)}; }
@@ -194,10 +199,9 @@ template <typename T> __device__ __forceinline__ uint32_t word_max(uint32_t a, u
 // Thread (col, slot) owns VEC channels of the rows slot, slot + NSLOT, ...: the split of
 // summaries_kernel, whose sums are repeated here in the same order bit for bit.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) pack_kernel(const T *__restrict__ k, const T *__restrict__ v,
-                                                        long long head_stride, int n_chunks, int first_chunk,
-                                                        uint8_t *__restrict__ hist, long long cap,
-                                                        float *__restrict__ summ, long long summ_cap) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
+    pack_kernel(const T *__restrict__ k, const T *__restrict__ v, long long head_stride, int n_chunks, int first_chunk,
+                uint8_t *__restrict__ hist, long long cap, float *__restrict__ summ, long long summ_cap) {
     using P = Packed<D>;
     constexpr int VEC = Vec16<T>::N;
     constexpr int LPR = D / VEC;
@@ -256,7 +260,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) pack_kernel(
         }
 #pragma unroll
         for (int e = 0; e < VEC; e += 4)
-            *reinterpret_cast<float4 *>(&part_sum[slot][col + e]) = make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
+            *reinterpret_cast<float4 *>(&part_sum[slot][col + e]) =
+                make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
         *reinterpret_cast<uint4 *>(&part_mn[slot][4 * lane_col]) = mn;
         *reinterpret_cast<uint4 *>(&part_mx[slot][4 * lane_col]) = mx;
     }
@@ -431,8 +436,9 @@ __device__ __forceinline__ void load4(const void *p, uint32_t (&r)[4]) {
     r[3] = v.w;
 }
 
-// One CTA per record, bound by the bytes it writes.  K words are 8 channels of a token,
-// one 16-byte store (bf16) each; a V thread turns 8 channels x 8 tokens in registers.
+// One CTA per record, bound by the bytes it writes (12.5 us for 1,792 bf16 chunks of
+// D = 128, 75 MB).  K words are 8 channels of a token, one 16-byte store (bf16) each; a V
+// thread turns 8 channels x 8 tokens in registers.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) unpack_kernel(const uint8_t *__restrict__ hist, long long cap,
                                                           int first_chunk, int n_chunks, T *__restrict__ k,

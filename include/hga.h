@@ -606,7 +606,8 @@ hga_status_t hga_qk_norm_rope(const hga_proj_t *p, const void *q, const void *k,
  *     zeros.  dq_weight, dk_weight: device fp32 [D], overwritten.
  *   q, k, weights, table, positions: the forward's.  kv_head_stride is not used.
  *   workspace: device, >= hga_qk_norm_rope_workspace_size(p) bytes, 16-byte aligned
- *     (partial sums of dw; nothing in it needs clearing).
+ *     (partial sums of dw; nothing in it needs clearing; calls in flight at the same
+ *     time, two captured graphs among them, need one each).
  * Two kernels; no atomics, so equal inputs give equal bits. */
 size_t hga_qk_norm_rope_workspace_size(const hga_proj_t *p);
 hga_status_t hga_qk_norm_rope_bwd(const hga_proj_t *p, const void *q, const void *k, const void *q_weight,
@@ -629,7 +630,7 @@ hga_status_t hga_qk_norm_rope_bwd(const hga_proj_t *p, const void *q, const void
  *   s = bf16(fl32(fl32(mx - mn) / 15)), 0 if below 2^-100;  z = bf16(fl32(mn - 16 s));
  *   c = the code nearest to the element, fl32(x - z) / s - 16 rounded to even in 0 .. 15.
  * So a value is off by at most half a step s/2, the roundings of z and of the value
- * (2^-9 |z| and 2^-9 |value|) and, at the ends, the range that rounding s lost.  A group
+ * (2^-8 |z| and 2^-8 |value|) and, at the ends, the range that rounding s lost.  A group
  * with an element that is not finite (or whose s or z overflows) reads back as NaN.
  *   hist: device, 16-byte aligned, [B][Hkv][hist_cap_chunks] records.
  * The attention calls below attend exactly the values that hga_unpack_history

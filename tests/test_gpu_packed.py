@@ -489,3 +489,21 @@ def _layer_grad(x, wq, wk, cs, c, dout):
         loss = loss + (dout[0, g * G:(g + 1) * G, r].double() * (s.softmax(-1) @ vv)).sum()
     loss.backward()
     return f64(x.grad), f64(wq.grad), f64(wk.grad)
+
+
+def test_readme_example():
+    """The README's code runs as printed."""
+    import os
+    import re
+    import hierarchical_sparse_long_b200 as hga
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")).read()
+    names = {}
+    for block in re.findall(r"```python\n(.*?)```", text, flags=re.S):
+        exec(block, names)
+    torch.cuda.synchronize()
+    assert hga.hga_get_device_status() == 0
+    assert torch.isfinite(names["out"]).all() and torch.isfinite(names["lse"]).all()
+    B, Hkv, nc, D = names["B"], names["Hkv"], names["nc"], names["D"]
+    want = torch.empty(B, Hkv, nc, D, device="cuda")
+    hga.hga_build_summaries(names["k_all"], names["L"], B, Hkv, D, 64, 0, nc, want, nc)
+    assert torch.equal(names["summ"][:, :, :nc], want)

@@ -229,8 +229,9 @@ def test_packed_attention_refused_by_form(L):
 def test_binding_raises():
     import torch
     t = torch.empty(4096, dtype=torch.uint8)
-    with pytest.raises(hga.HGAError):
-        hga.hga_attn_decode_packed(hga.Params(**{**ATTN, "seg_len": 1, "q_block": 1}), t, t, 7, t, t, 1, t, t, t, stream=0)
+    p = hga.Params(**{**ATTN, "seg_len": 1, "q_block": 1})
+    with pytest.raises(hga.HGAError):  # seven records of a history of eight
+        hga.hga_attn_decode_packed(p, t, t, 7, t, t, 1, t, t, t, stream=0)
 
 
 def test_params_struct_follows_the_fields():
