@@ -38,6 +38,7 @@
 // keys); a half's softmax (about 1,500) and products overlap with the other half's.  128-token
 // tiles, which re-read the queries half as often, left room for one score buffer per half and
 // took 2,300 cycles per 64 tokens: softmax and products of a half no longer overlap.
+#include "dependent.cuh"
 #include "packed.cuh"
 #include "tc_issue.cuh"
 #include "tc_ptx.cuh"
@@ -232,6 +233,8 @@ __global__ void __launch_bounds__(32 * (kIssueWarps + 4 * NH + kProdWarps), 1)
         bars->abort = 0;
         tc::fence_mbar_init();
     }
+    if (warp == 0) tc::tmem_alloc<512>(&bars->tmem_base);
+    depend_wait();
     if (warp == 1) {  // the block's valid routes, in order; -1 is padding, anything else is skipped and flagged
         const int32_t *sel = a.idx + ((long long)bg * nqb + m) * a.topk;
         int n = 0;
@@ -246,7 +249,6 @@ __global__ void __launch_bounds__(32 * (kIssueWarps + 4 * NH + kProdWarps), 1)
         }
         if (lane == 0) bars->n_hist = n;
     }
-    if (warp == 0) tc::tmem_alloc<512>(&bars->tmem_base);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -549,6 +551,7 @@ __global__ void __launch_bounds__(32 * (kIssueWarps + 4 * NH + kProdWarps), 1)
         if (ok && __all_sync(0xffffffffu, tc::mbar_wait(&bars->o_done[h][(n_tiles - 1) & 1],
                                                         ((n_tiles - 1) >> 1) & 1, abort, a.status))) {
             tc::fence_after_sync();
+            depend_next();
             const bool write = hh < a.hc;  // rows 64..127 repeat the head when HC = 1
             const long long row = ((long long)(b * a.n_q_heads + h0 + (write ? hh : 0))) * a.seg_len + m * TILE + i;
             const float inv_l = 1.f / l_run;
@@ -665,8 +668,8 @@ hga_status_t launch_nh(const hga_params_t &p, const void *q, const uint8_t *hist
     // segment: 265 -> 254 us; 256 CTAs of the 16K segment: 74.5 -> 76 us, so not there).
     const unsigned sms = (unsigned)sm_count();
     a.n_first = grid >= 2 * sms ? (int)(grid % sms) : 0;
-    kern<<<grid, 32 * (kIssueWarps + 4 * NH + kProdWarps), Smem<D, NH>::ALLOC, stream>>>(mq, mks, mvs, mo, a);
-    return record_cuda(cudaGetLastError());
+    return record_cuda(launch_dependent(kern, grid, 32 * (kIssueWarps + 4 * NH + kProdWarps), Smem<D, NH>::ALLOC, 1,
+                                        stream, mq, mks, mvs, mo, a));
 }
 
 }  // namespace

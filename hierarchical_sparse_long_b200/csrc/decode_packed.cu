@@ -34,6 +34,7 @@
 // then by cluster, the 16 sequences took 19.6 us.
 #include <cstddef>
 
+#include "dependent.cuh"
 #include "packed.cuh"
 #include "tc_ptx.cuh"
 
@@ -49,6 +50,7 @@ constexpr int kMaxRouted = 64;  // topk limit of the parameter check
 constexpr int kHeads = 8;       // query heads per KV head: the N side of the products
 constexpr int kMaxCluster = 8;  // portable cluster size
 constexpr int kCtasPerSm = 3;   // 168 registers a thread, 74 KiB of rings a CTA
+constexpr unsigned kSmBytes = 228 * 1024;  // shared memory of an SM
 constexpr int kStages = 2;      // one unit multiplied, one on its way
 
 struct PackedDecodeArgs {
@@ -125,6 +127,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_packed_kernel(con
     const int bg = (int)blockIdx.x / a.n_cluster;
     const int b = bg / a.n_kv_heads, g = bg % a.n_kv_heads;
 
+    depend_wait();
     // queries of head r as the B operand: pair p of octet j of the lane's channels
     uint32_t qf[NJ][4];
 #pragma unroll
@@ -344,6 +347,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_packed_kernel(con
         }
         __syncwarp();  // every lane has read the stage
     }
+    depend_next();
     __syncthreads();  // the rings are free
 
     // this warp's maximum, sum and output
@@ -446,23 +450,16 @@ int cluster_size(const hga_params_t &p, int n_local) {
 }
 
 template <int D> hga_status_t launch_d(const PackedDecodeArgs &a, unsigned bg, cudaStream_t stream) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(bg * a.n_cluster);
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = a.n_cluster;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    constexpr int smem = kWarps * kStages * Packed<D>::kRecord;
-    cfg.dynamicSmemBytes = smem;
-    cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(decode_packed_kernel<D>), smem);
+    // The CTAs come to SMs that the previous kernel leaves one after another; with room for
+    // more of them than their even share, the first SMs take too many (16.1 against 14.3 us
+    // per call of 256 CTAs in a graph).  So each asks for more than a (share + 1)-th of the
+    // shared memory.
+    const unsigned grid = bg * a.n_cluster, sms = (unsigned)sm_count(), share = (grid + sms - 1) / sms;
+    int smem = kWarps * kStages * Packed<D>::kRecord;
+    if (share <= kCtasPerSm && smem < (int)(kSmBytes / (share + 1))) smem = (int)(kSmBytes / (share + 1));
+    const cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void *>(decode_packed_kernel<D>), smem);
     if (e != cudaSuccess) return record_cuda(e);
-    e = cudaLaunchKernelEx(&cfg, decode_packed_kernel<D>, a);
-    if (e == cudaSuccess) e = cudaGetLastError();
-    return record_cuda(e);
+    return record_cuda(launch_dependent(decode_packed_kernel<D>, grid, kThreads, smem, a.n_cluster, stream, a));
 }
 
 }  // namespace

@@ -24,6 +24,7 @@
 // CTAs of their own, at twice the CTAs, took 10 us more.
 #include <cfloat>
 
+#include "dependent.cuh"
 #include "packed.cuh"
 
 namespace hga {
@@ -222,6 +223,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
     const long long row0 = slice * head_stride + (long long)j * kChunk;
     uint8_t *rec = hist + (slice * cap + first_chunk + j) * P::kRecord;
 
+    depend_wait();
     // the rows as they lie in memory; widened where they are used
     uint4 xr[ROWS], yr[ROWS];
 #pragma unroll
@@ -361,6 +363,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
         }
     }
 
+    depend_next();
+
     // V codes: four channels x eight tokens per step, turned in registers
     uint32_t *vw = reinterpret_cast<uint32_t *>(rec + P::kPart);
     for (int i = tid; i < 2 * D; i += kThreads) {
@@ -450,6 +454,8 @@ __global__ void __launch_bounds__(kThreads) unpack_kernel(const uint8_t *__restr
     const int j = (int)(blockIdx.x % n_chunks);
     const uint8_t *rec = hist + (slice * cap + first_chunk + j) * P::kRecord;
     const long long row0 = slice * head_stride + (long long)j * kChunk;
+    depend_wait();
+    depend_next();
     if (tid < kThreads / 2) {
         const int o = tid % OPR;
         uint32_t s[4], z[4], r[4];
@@ -487,18 +493,17 @@ __global__ void __launch_bounds__(kThreads) unpack_kernel(const uint8_t *__restr
 template <typename T, int D>
 hga_status_t pack_t(const void *k, const void *v, long long head_stride, long long slices, int first_chunk,
                     int n_chunks, uint8_t *hist, int cap, float *summ, int summ_cap, cudaStream_t stream) {
-    pack_kernel<T, D><<<(unsigned)(slices * n_chunks), kThreads, 0, stream>>>(
-        static_cast<const T *>(k), static_cast<const T *>(v), head_stride, n_chunks, first_chunk, hist, cap, summ,
-        summ_cap);
-    return record_cuda(cudaGetLastError());
+    return record_cuda(launch_dependent(pack_kernel<T, D>, (unsigned)(slices * n_chunks), kThreads, 0, 1, stream,
+                                        static_cast<const T *>(k), static_cast<const T *>(v), head_stride, n_chunks,
+                                        first_chunk, hist, cap, summ, summ_cap));
 }
 
 template <typename T, int D>
 hga_status_t unpack_t(const uint8_t *hist, int cap, long long slices, int first_chunk, int n_chunks, void *k, void *v,
                       long long head_stride, cudaStream_t stream) {
-    unpack_kernel<T, D><<<(unsigned)(slices * n_chunks), kThreads, 0, stream>>>(
-        hist, cap, first_chunk, n_chunks, static_cast<T *>(k), static_cast<T *>(v), head_stride);
-    return record_cuda(cudaGetLastError());
+    return record_cuda(launch_dependent(unpack_kernel<T, D>, (unsigned)(slices * n_chunks), kThreads, 0, 1, stream,
+                                        hist, cap, first_chunk, n_chunks, static_cast<T *>(k), static_cast<T *>(v),
+                                        head_stride));
 }
 
 }  // namespace

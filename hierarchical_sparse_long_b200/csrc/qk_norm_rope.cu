@@ -23,6 +23,7 @@
 // 10.7 us (50 MB, 4.8 TB/s), backward 22.4 us (98 MB, 4.4 TB/s); with scalar arithmetic and
 // loads behind the position's they took 16.6 and 33.1 us.
 #include "common.cuh"
+#include "dependent.cuh"
 
 namespace hga {
 
@@ -186,6 +187,7 @@ __global__ void __launch_bounds__(kThreads, HPT == 1 ? 8 : 5) norm_rope_kernel(c
     int e0, e1;
     const bool rotated = lane_vectors<VEC>(a, l, e0, e1);
 
+    depend_wait();
     uint4 x[HPT][2];
     const T *src = static_cast<const T *>(a.x[kind]) + t * a.x_stride[kind] + h0 * D;
 #pragma unroll
@@ -214,6 +216,7 @@ __global__ void __launch_bounds__(kThreads, HPT == 1 ? 8 : 5) norm_rope_kernel(c
     const Pr w0 = Pr::widen(*reinterpret_cast<const uint4 *>(wp + e0));
     const Pr w1 = Pr::widen(*reinterpret_cast<const uint4 *>(wp + e1));
     const Turn<T> turn(a, pos, e0, rotated && pos >= 0);
+    depend_next();
 #pragma unroll
     for (int h = 0; h < HPT; ++h) {
         Pr x0 = Pr::widen(x[h][0]), x1 = Pr::widen(x[h][1]);
@@ -250,8 +253,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) norm_rope_bwd_kernel(const
     const long long n_tok = (long long)a.batch * a.seq_len;
     int e0, e1;
     const bool rotated = lane_vectors<VEC>(a, l, e0, e1);
-    // norm_rope_dw may take its place beside this kernel's last CTAs
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    depend_wait();
     Pr dw0 = Pr::fill(0.f), dw1 = dw0;
     uint4 wr[2] = {};
     if (kind < 2) {
@@ -320,6 +322,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) norm_rope_bwd_kernel(const
             }
         }
     }
+    depend_next();
     if (kind == 2) return;
 #pragma unroll
     for (int j = 0; j < Pr::N; ++j) {
@@ -338,15 +341,15 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) norm_rope_bwd_kernel(const
 }
 
 // dw of q (blockIdx.y = 0) and k (1): the partials of its head groups, in a fixed order, in
-// 64 bits.  A CTA takes 8 dims with 32 threads each.  Launched while the backward kernel
-// still runs; what it sums is there once the wait returns.
+// 64 bits.  A CTA takes 8 dims with 32 threads each.
 template <int D>
 __global__ void __launch_bounds__(256) norm_rope_dw(const NormRopeArgs a, int grid_x) {
     __shared__ double part[8][8];
     const int kind = blockIdx.y, d = threadIdx.x % 8, slot = threadIdx.x / 8;
     const long long n = (long long)a.groups[kind] * grid_x;
     const float *p = a.partial + (kind ? (long long)a.groups[0] * grid_x * D : 0) + blockIdx.x * 8 + d;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    depend_wait();
+    depend_next();
     double sum = 0.0;
 #pragma unroll 8
     for (long long i = slot; i < n; i += 32) sum += (double)p[i * D];
@@ -412,14 +415,10 @@ template <typename T, int D> hga_status_t launch_fwd(NormRopeArgs a, cudaStream_
     const long long n_tok = (long long)a.batch * a.seq_len;
     const long long gx = (n_tok + slots - 1) / slots;
     set_groups(a, kHeads);
-    if (gx * (a.groups[0] + 2 * a.groups[1]) >= 2 * sm_count()) {
-        norm_rope_kernel<T, D, kHeads>
-            <<<dim3((unsigned)gx, a.groups[0] + 2 * a.groups[1]), kThreads, 0, stream>>>(a);
-    } else {
-        set_groups(a, 1);
-        norm_rope_kernel<T, D, 1><<<dim3((unsigned)gx, a.groups[0] + 2 * a.groups[1]), kThreads, 0, stream>>>(a);
-    }
-    return record_cuda(cudaGetLastError());
+    const bool longer = gx * (a.groups[0] + 2 * a.groups[1]) >= 2 * sm_count();
+    if (!longer) set_groups(a, 1);
+    return record_cuda(launch_dependent(longer ? norm_rope_kernel<T, D, kHeads> : norm_rope_kernel<T, D, 1>,
+                                        dim3((unsigned)gx, a.groups[0] + 2 * a.groups[1]), kThreads, 0, 1, stream, a));
 }
 
 // CTAs along the tokens of the backward: one wave of 148 SMs over all head groups.  A
@@ -435,19 +434,10 @@ long long bwd_grid_x(const hga_proj_t &p) {
 
 template <typename T, int D> hga_status_t launch_bwd(NormRopeArgs a, long long gx, cudaStream_t stream) {
     set_groups(a, kHeads);
-    norm_rope_bwd_kernel<T, D><<<dim3((unsigned)gx, a.groups[0] + 2 * a.groups[1]), kThreads, 0, stream>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    const dim3 grid((unsigned)gx, a.groups[0] + 2 * a.groups[1]);
+    const cudaError_t e = launch_dependent(norm_rope_bwd_kernel<T, D>, grid, kThreads, 0, 1, stream, a);
     if (e != cudaSuccess) return record_cuda(e);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(D / 8, 2);
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return record_cuda(cudaLaunchKernelEx(&cfg, norm_rope_dw<D>, a, (int)gx));
+    return record_cuda(launch_dependent(norm_rope_dw<D>, dim3(D / 8, 2), 256, 0, 1, stream, a, (int)gx));
 }
 
 }  // namespace

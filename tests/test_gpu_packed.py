@@ -507,3 +507,70 @@ def test_readme_example():
     want = torch.empty(B, Hkv, nc, D, device="cuda")
     hga.hga_build_summaries(names["k_all"], names["L"], B, Hkv, D, 64, 0, nc, want, nc)
     assert torch.equal(names["summ"][:, :, :nc], want)
+
+
+@pytest.mark.parametrize("mode", ["stream", "graph"])
+def test_calls_behind_one_another(mode):
+    """Each kernel takes its place while the previous one drains.  A run of calls in which each
+    reads what the one before wrote, and writes what the one before read, gives the bits of the
+    same run with the device idle between any two calls."""
+    import hierarchical_sparse_long_b200 as hga
+    B, Hq, Hkv, D, topk, steps = 2, 16, 4, 128, 3, 4
+    rng = np.random.default_rng(31)
+    row = (Hq + 2 * Hkv) * D
+    x = host(rng.standard_normal((steps, B, 64, row)))
+    w = host(1 + 0.1 * rng.standard_normal(D))
+    table = torch.empty(512, D, device="cuda")
+    hga.hga_rope_table(1e6, D, 512, table)
+    dq, dk, dv = (host(rng.standard_normal((B, h, 64, D)), torch.float32) for h in (Hq, Hkv, Hkv))
+    buf = lambda *s, t=BF16: torch.zeros(*s, device="cuda", dtype=t)
+    q, k, v = buf(B, Hq, 64, D), buf(B, Hkv, 64, D), buf(B, Hkv, 64, D)
+    hist = buf(B, Hkv, steps, 72 * D, t=torch.uint8)
+    summ, idx = buf(B, Hkv, steps, D, t=torch.float32), buf(B, Hkv, 1, topk, t=torch.int32)
+    out, lse = buf(B, Hq, 64, D), buf(B, Hq, 64, t=torch.float32)
+    one, lse1 = buf(B, Hq, 1, D), buf(B, Hq, 1, t=torch.float32)
+    q1, k2, v2 = buf(B, Hq, 1, D), buf(B, Hkv, 64, D), buf(B, Hkv, 64, D)
+    dx, dw = buf(B, 64, row), buf(2, D, t=torch.float32)
+    p = hga.ProjParams(B, Hq, Hkv, D, 64, D)
+    ws = buf(hga.hga_qk_norm_rope_workspace_size(p), t=torch.uint8)
+    seen = buf(steps, B, Hq, 64, D), buf(steps, B, Hq, 1, D), buf(steps, B, 64, row), buf(steps, 2, D, t=torch.float32)
+
+    def run(idle):
+        for i in range(steps):
+            a = x[i]
+            f = hga.Params(B, Hq, Hkv, D, topk, 64, i)
+            d = hga.Params(B, Hq, Hkv, D, topk, 1, i + 1, seg_head_stride=64, q_block=1)
+            for call in (
+                    lambda: hga.hga_qk_norm_rope(p, a, a[..., Hq * D:], a[..., (Hq + Hkv) * D:], w, w, table, None, q,
+                                                 k, v),
+                    lambda: hga.hga_route(f, q, summ, steps, idx),
+                    lambda: hga.hga_attn_fwd_packed(f, q, hist, steps, k, v, idx, out, lse),
+                    lambda: hga.hga_pack_history(k, v, 64, B, Hkv, D, i, 1, hist, steps, summ, steps),
+                    lambda: hga.hga_unpack_history(hist, steps, B, Hkv, D, i, 1, k2, v2, 64),
+                    lambda: q1.copy_(out[:, :, 63:]),
+                    lambda: hga.hga_route(d, q1, summ, steps, idx),
+                    lambda: hga.hga_attn_decode_packed(d, q1, hist, steps, k2, v2, 33, idx, one, lse1),
+                    lambda: hga.hga_qk_norm_rope_bwd(p, a, a[..., Hq * D:], w, w, table, None, dq, dk, dv, dx,
+                                                     dx[..., Hq * D:], dx[..., (Hq + Hkv) * D:], dw[0], dw[1], ws),
+                    lambda: dq.copy_(q),
+                    lambda: [s[i].copy_(t) for s, t in zip(seen, (out, one, dx, dw))]):
+                call()
+                if idle:
+                    torch.cuda.synchronize()
+
+    start = dq.clone()
+    run(True)
+    want = [s.clone() for s in seen]
+    assert all(torch.isfinite(t).all() for t in want)
+    graph = torch.cuda.CUDAGraph()
+    if mode == "graph":
+        with torch.cuda.graph(graph):
+            run(False)
+    for _ in range(5):
+        dq.copy_(start)
+        for t in (q, k, v, hist, summ, idx, out, one, q1, k2, v2, dx, dw, *seen):
+            t.zero_()
+        graph.replay() if mode == "graph" else run(False)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(seen, want))
+    del graph
