@@ -31,8 +31,9 @@
 // TMEM (512 columns): O_h at 128h, S_h double-buffered at 256 + 128h + 64b.
 // Every wait is bounded; a timeout sets HGA_DEV_TIMEOUT and the CTA unwinds.
 //
-// Measured: 74.8 us for the last 2,048 queries of 16K (32 + 8 heads, 68.7 GFLOP: 919
-// TFLOP/s), 254 us for the last 4,096 of 128K (275 GFLOP: 1,083 TFLOP/s).  A 64-token tile of
+// Measured: 74.1 us for the last 2,048 queries of 16K (32 + 8 heads, 68.7 GFLOP: 927
+// TFLOP/s), 254 us for the last 4,096 of 128K (275 GFLOP: 1,083 TFLOP/s), in bursts; for
+// seconds on end the power cap makes them 80.5 and 291 us.  A 64-token tile of
 // two halves takes about 1,950 cycles, of which its products' operand traffic from shared
 // memory accounts for about 1,470 (a QK product re-reads its 128 rows of queries for 64
 // keys); a half's softmax (about 1,500) and products overlap with the other half's.  128-token

@@ -26,8 +26,8 @@
 // output, which are merged through shared memory, first of the CTA, then of the
 // cluster: one launch, no workspace, sums in a fixed order.
 //
-// Measured: 13.9 us for 16 sequences of 32 + 8 heads at 32 routed chunks and 64 window tokens
-// (42 MB, 3.0 TB/s of the 6.5 that a copy reaches), 5.0 us for one at 16 chunks.  A unit is
+// Measured: 13.8 us for 16 sequences of 32 + 8 heads at 32 routed chunks and 64 window tokens
+// (42 MB, 3.1 TB/s of the 6.5 that a copy reaches), 4.9 us for one at 16 chunks.  A unit is
 // about 1,040 instructions, half of them shifts and masks of the integer pipe, which two or
 // three warps of a scheduler keep busy; the rest is the start (routes, then first records)
 // and the merge.  With loads into registers in place of the ring, and a merge by CTA and

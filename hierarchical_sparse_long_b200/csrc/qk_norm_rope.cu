@@ -20,7 +20,7 @@
 // the rotation stays inside a thread and only the mean crosses lanes.  A CTA takes a few
 // heads (gridDim.y) of a run of tokens: its reads are whole 128-byte lines of token rows,
 // its writes consecutive rows of a head.  2,048 tokens of 32 + 8 heads of 128 in bf16: forward
-// 10.7 us (50 MB, 4.8 TB/s), backward 22.4 us (98 MB, 4.4 TB/s); with scalar arithmetic and
+// 10.6 us (50 MB, 4.8 TB/s), backward 21.8 us (98 MB, 4.5 TB/s); with scalar arithmetic and
 // loads behind the position's they took 16.6 and 33.1 us.
 #include "common.cuh"
 #include "dependent.cuh"

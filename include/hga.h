@@ -592,6 +592,8 @@ hga_status_t hga_rope_table(double theta, int rotary_dim, long long n_pos, float
  *     kv_head_stride tokens apart: rows [0, S) of each are written, so a pointer
  *     into a segment or local-window buffer appends the tokens to it.  Outputs
  *     must not overlap inputs.
+ * A buffer that attention reads in whole tiles (hga_attn_fwd multiplies the V rows behind
+ * a query by zero) wants finite rows there: clear it once if padding rows end up in it.
  * S = 1 is the step of a new token of every sequence.  One kernel. */
 hga_status_t hga_qk_norm_rope(const hga_proj_t *p, const void *q, const void *k, const void *v, const void *q_weight,
                               const void *k_weight, const float *table, long long n_pos, const int32_t *positions,
