@@ -515,7 +515,7 @@ def test_calls_behind_one_another(mode):
     reads what the one before wrote, and writes what the one before read, gives the bits of the
     same run with the device idle between any two calls."""
     import hierarchical_sparse_long_b200 as hga
-    B, Hq, Hkv, D, topk, steps = 2, 16, 4, 128, 3, 4
+    B, Hq, Hkv, D, topk, steps = 2, 12, 3, 128, 3, 4
     rng = np.random.default_rng(31)
     row = (Hq + 2 * Hkv) * D
     x = host(rng.standard_normal((steps, B, 64, row)))
