@@ -6,8 +6,8 @@
 //
 // Grid of a group with extremes mn, mx (K: a channel's 64 tokens, V: 64 channels of a
 // token), c nearest to the value, ties to even:
-//   s = bf16(fl(fl(mx - mn) / 15)), 0 below 2^-100
-//   z = bf16(fl(mn - 16 s)),   c = clamp(rne(fl(x - z) / s) - 16, 0, 15), 0 where s = 0
+//   s = bf16(fl(fl(mx - mn) fl(1 / 15))), 0 below 2^-100
+//   z = bf16(fl(mn - 16 s)),   c = clamp(rne((x - z) / s) - 16, 0, 15), 0 where s = 0
 // s and z are rounded first and the codes chosen for the rounded grid, so their
 // rounding moves the grid and not the choice.  s = z = NaN when an element is not finite
 // (the extremes propagate NaN, an infinity makes s infinite) or s or z is not: the
@@ -42,7 +42,7 @@ __device__ __forceinline__ float bf16_round(float x) { return __bfloat162float(_
 
 __device__ __forceinline__ Grid make_grid(float mn, float mx) {
     Grid g;
-    g.s = bf16_round(__fdiv_rn(mx - mn, 15.f));
+    g.s = bf16_round(__fmul_rn(__fsub_rn(mx, mn), 1.f / 15.f));
     if (g.s < 0x1p-100f) g.s = 0.f;
     g.z = bf16_round(fmaf(-16.f, g.s, mn));
     // fabsf(NaN) <= FLT_MAX is false
@@ -82,8 +82,10 @@ template <bool kNibble> __device__ constexpr int code_shift(int e) {
 // [0, 1] and 15 p is within 2^-17 of the quotient.  Rounding it to 2^-14 turns what lies that
 // close to a border into a tie, which the rounding to an integer (adding 1.5 2^23 leaves the
 // integer in the low bits) gives to the even code.  A true tie belongs there; an element
-// that does not is more than half a step from its code, and r = x - z - (16 + c) s tells,
-// exactly: r[e] is for the caller to compare with s / 2.
+// that does not is more than half a step from its code, and r = x - ((16 + c) s + z) tells:
+// the sum is exact (14 bits of the product against 8 of z) unless z is beyond 2^16 s or,
+// other than zero, below 2^-12 s, and so is the difference of two numbers this close.  r[e]
+// is for the caller to compare with s / 2.
 template <int N, bool kNibble>
 __device__ __forceinline__ uint32_t codes(const float (&x)[N], const float (&ss)[N], const float (&zs)[N],
                                           const float (&inv)[N], float (&r)[N]) {
@@ -98,7 +100,8 @@ __device__ __forceinline__ uint32_t codes(const float (&x)[N], const float (&ss)
         const float2 u = __ffma2_rn(p, make_float2(15.f, 15.f), make_float2(magic14, magic14));
         const float2 t = __fadd2_rn(u, make_float2(magic - magic14, magic - magic14));
         const float2 k = __fadd2_rn(t, make_float2(16.f - magic, 16.f - magic));
-        const float2 d = __ffma2_rn(k, make_float2(-ss[e], -ss[e + 1]), y);
+        const float2 g = __ffma2_rn(k, make_float2(-ss[e], -ss[e + 1]), make_float2(-zs[e], -zs[e + 1]));
+        const float2 d = __fadd2_rn(make_float2(x[e], x[e + 1]), g);
         r[e] = d.x;
         r[e + 1] = d.y;
         // the constant bits of t add up to a constant, modulo 2^32
@@ -109,14 +112,13 @@ __device__ __forceinline__ uint32_t codes(const float (&x)[N], const float (&ss)
     return w - off;
 }
 
-// A code, at most one off, decided by the exact borders (16 + k +- 1/2) s (6 bits x 8 bits).
+// A code, at most one off, decided by its borders (16 + k +- 1/2) s + z.
 __device__ __forceinline__ uint32_t exact_code(float x, const Grid &g, uint32_t k) {
-    const float y = __fsub_rn(x, g.z);
-    const float up = (16.5f + (float)k) * g.s, dn = (15.5f + (float)k) * g.s;
+    const float up = fmaf(16.5f + (float)k, g.s, g.z), dn = fmaf(15.5f + (float)k, g.s, g.z);
     const bool odd = k & 1;
-    if (y > up || (y == up && odd))
+    if (x > up || (x == up && odd))
         k = k < 15u ? k + 1u : k;
-    else if (y < dn || (y == dn && odd))
+    else if (x < dn || (x == dn && odd))
         k = k > 0u ? k - 1u : k;
     // a NaN grid fails every comparison and keeps code 0; s = 0 has only code 0
     return g.s == 0.f ? 0u : k;

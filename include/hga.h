@@ -629,8 +629,8 @@ hga_status_t hga_qk_norm_rope_bwd(const hga_proj_t *p, const void *q, const void
  * Nibble j < 4 of a word is its element 2j, nibble 4 + j its element 2j + 1.  Code c
  * stands for bf16(s (16 + c) + z), rounded once.  For a group (one pair's elements)
  * with extremes mn, mx:
- *   s = bf16(fl32(fl32(mx - mn) / 15)), 0 if below 2^-100;  z = bf16(fl32(mn - 16 s));
- *   c = the code nearest to the element, fl32(x - z) / s - 16 rounded to even in 0 .. 15.
+ *   s = bf16(fl32(fl32(mx - mn) fl32(1/15))), 0 if below 2^-100;  z = bf16(fl32(mn - 16 s));
+ *   c = the code nearest to the element, (x - z) / s - 16 rounded to even in 0 .. 15.
  * So a value is off by at most half a step s/2, the roundings of z and of the value
  * (2^-8 |z| and 2^-8 |value|) and, at the ends, the range that rounding s lost.  A group
  * with an element that is not finite (or whose s or z overflows) reads back as NaN.

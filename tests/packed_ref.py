@@ -65,14 +65,13 @@ def quant(x, axis):
     """Grid (s, z) and codes of x (bf16 or fp32 values as float64) in groups along axis."""
     with np.errstate(all="ignore"):
         mn, mx = x.min(axis, keepdims=True), x.max(axis, keepdims=True)
-        spread = (mx - mn).astype(np.float32)  # rounded to fp32, as is the quotient
-        s = to_bf16((spread / np.float32(15)).astype(np.float64))
+        spread = (mx - mn).astype(np.float32)  # rounded to fp32, as are 1/15 and the product
+        s = to_bf16((spread * np.float32(1 / 15)).astype(np.float64))
         s = np.where(s < 2.0 ** -100, 0.0, s)
         z = to_bf16((mn - 16 * s).astype(np.float32).astype(np.float64))
         bad = ~np.isfinite(x).all(axis, keepdims=True) | ~np.isfinite(s) | ~np.isfinite(z)
         s, z = np.where(bad, np.nan, s), np.where(bad, np.nan, z)
-        y = (x - z).astype(np.float32).astype(np.float64)  # rounded to fp32
-        c = np.clip(np.rint(y / np.where(s == 0, 1.0, s)), 16, 31) - 16
+        c = np.clip(np.rint((x - z) / np.where(s == 0, 1.0, s)), 16, 31) - 16
         c = np.where((s == 0) | bad, 0, c).astype(np.int64)
     return s, z, c
 
