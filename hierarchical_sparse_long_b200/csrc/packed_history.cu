@@ -398,12 +398,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
     uint32_t kw[ROWS];
     float far[VEC];
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-        float x[VEC], d[VEC];
+    for (int r = 0; r < ROWS; r += 2) {  // two rows: their distances meet in a three-way maximum
+        float x[VEC], d[2][VEC];
         widen(xr[r], x);
-        kw[r] = codes<VEC, true>(x, ss, zs, iv, d);
+        kw[r] = codes<VEC, true>(x, ss, zs, iv, d[0]);
+        widen(xr[r + 1], x);
+        kw[r + 1] = codes<VEC, true>(x, ss, zs, iv, d[1]);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) far[e] = r ? fmaxf(far[e], fabsf(d[e])) : fabsf(d[e]);
+        for (int e = 0; e < VEC; ++e) far[e] = fmaxf(fmaxf(r ? far[e] : 0.f, fabsf(d[0][e])), fabsf(d[1][e]));
     }
     bool redo = false;
 #pragma unroll

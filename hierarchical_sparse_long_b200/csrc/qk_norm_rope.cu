@@ -142,9 +142,9 @@ template <int VEC> __device__ __forceinline__ bool lane_vectors(const NormRopeAr
     return rotated;
 }
 
-// cos, sin and -sin of a lane's pairs.
+// cos and sin of a lane's pairs.
 template <typename T> struct Turn {
-    Pairs<T> c, s, ns;
+    Pairs<T> c, s;
     __device__ __forceinline__ Turn(const NormRopeArgs &a, long long pos, int e0, bool rotated) {
         c = Pairs<T>::fill(1.f);
         s = Pairs<T>::fill(0.f);
@@ -153,8 +153,6 @@ template <typename T> struct Turn {
             c = Pairs<T>::load_f32(row);
             s = Pairs<T>::load_f32(row + a.rot / 2);
         }
-#pragma unroll
-        for (int i = 0; i < Pairs<T>::N; ++i) ns.v[i] = minus(s.v[i]);
     }
 };
 
@@ -225,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, HPT == 1 ? 8 : 5) norm_rope_kernel(c
         for (int j = 0; j < Pr::N; ++j) {
             const float2 n0 = __fmul2_rn(__fmul2_rn(x0.v[j], r), w0.v[j]);
             const float2 n1 = __fmul2_rn(__fmul2_rn(x1.v[j], r), w1.v[j]);
-            x0.v[j] = __ffma2_rn(n1, turn.ns.v[j], __fmul2_rn(n0, turn.c.v[j]));
+            x0.v[j] = __ffma2_rn(n0, turn.c.v[j], minus(__fmul2_rn(n1, turn.s.v[j])));
             x1.v[j] = __ffma2_rn(n0, turn.s.v[j], __fmul2_rn(n1, turn.c.v[j]));
         }
         if (pos >= 0 && h0 + h < n_heads) {
@@ -299,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas) norm_rope_bwd_kernel(const
 #pragma unroll
                     for (int j = 0; j < Pr::N; ++j) {
                         const float2 dn0 = __ffma2_rn(g1[h].v[j], turn.s.v[j], __fmul2_rn(g0[h].v[j], turn.c.v[j]));
-                        const float2 dn1 = __ffma2_rn(g0[h].v[j], turn.ns.v[j], __fmul2_rn(g1[h].v[j], turn.c.v[j]));
+                        const float2 dn1 = __ffma2_rn(g1[h].v[j], turn.c.v[j], minus(__fmul2_rn(g0[h].v[j], turn.s.v[j])));
                         x0.v[j] = __fmul2_rn(x0.v[j], both(r));
                         x1.v[j] = __fmul2_rn(x1.v[j], both(r));
                         dw0.v[j] = __ffma2_rn(dn0, x0.v[j], dw0.v[j]);
