@@ -531,12 +531,18 @@ def hga_packed_chunk_bytes(head_dim: int) -> int:
     return int(lib().hga_packed_chunk_bytes(head_dim))
 
 
+def _kv_dtype(k, v) -> int:
+    if k.dtype != v.dtype:  # both are read, or written, as k's
+        raise HGAError(-1, "k and v of different dtypes", f"{k.dtype}, {v.dtype}")
+    return dtype_code(k)
+
+
 def hga_pack_history(k, v, head_stride: int, batch: int, n_kv_heads: int, head_dim: int, first_chunk: int,
                      n_chunks: int, hist, hist_cap_chunks: int, summ=None, summ_cap_chunks: int = 0, stream=None):
     """Packs closed chunks (rows 0 .. of k / v) into the 4-bit records [first_chunk, first_chunk +
     n_chunks) of hist, and appends their summaries when summ is given."""
     _check(lib().hga_pack_history(_ptr(k), _ptr(v), head_stride, batch, n_kv_heads, head_dim, first_chunk, n_chunks,
-                                  dtype_code(k), _ptr(hist), hist_cap_chunks, _ptr(summ), summ_cap_chunks,
+                                  _kv_dtype(k, v), _ptr(hist), hist_cap_chunks, _ptr(summ), summ_cap_chunks,
                                   _stream(stream)), "hga_pack_history")
 
 
@@ -544,7 +550,7 @@ def hga_unpack_history(hist, hist_cap_chunks: int, batch: int, n_kv_heads: int, 
                        n_chunks: int, k, v, head_stride: int, stream=None):
     """The values of packed chunks [first_chunk, first_chunk + n_chunks) into rows 0 .. of k / v."""
     _check(lib().hga_unpack_history(_ptr(hist), hist_cap_chunks, batch, n_kv_heads, head_dim, first_chunk, n_chunks,
-                                    dtype_code(k), _ptr(k), _ptr(v), head_stride, _stream(stream)),
+                                    _kv_dtype(k, v), _ptr(k), _ptr(v), head_stride, _stream(stream)),
            "hga_unpack_history")
 
 

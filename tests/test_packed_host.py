@@ -234,6 +234,17 @@ def test_binding_raises():
         hga.hga_attn_decode_packed(p, t, t, 7, t, t, 1, t, t, t, stream=0)
 
 
+def test_binding_refuses_mixed_dtypes():
+    import torch
+    k, hist = torch.empty(64 * 64), torch.empty(4608, dtype=torch.uint8)
+    with pytest.raises(hga.HGAError, match="different dtypes"):
+        hga.hga_pack_history(k, k.bfloat16(), 64, 1, 1, 64, 0, 1, hist, 1, stream=0)
+    with pytest.raises(hga.HGAError, match="different dtypes"):
+        hga.hga_unpack_history(hist, 1, 1, 1, 64, 0, 1, k.bfloat16(), k, 64, stream=0)
+    with pytest.raises(hga.HGAError, match="unsupported tensor dtype"):
+        hga.hga_pack_history(k.half(), k.half(), 64, 1, 1, 64, 0, 1, hist, 1, stream=0)
+
+
 def test_params_struct_follows_the_fields():
     """The C struct of a Params is kept between calls and made anew after a change."""
     import copy
