@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import dataclasses
 import os
+import typing
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libhga.so")
@@ -51,20 +52,21 @@ class CParams(ctypes.Structure):
 
 
 class _Mirror:
-    """A dataclass whose C struct is built by the first call after a change of its fields."""
+    """A dataclass with a C struct: equal fields share one struct, so that a call does not
+    build it anew."""
+    _refs: typing.ClassVar[dict]
 
-    def __setattr__(self, name, value):
-        self.__dict__[name] = value
-        self.__dict__.pop("_ref", None)
+    def __init_subclass__(cls):
+        cls._refs = {}
 
     def ref(self):
-        r = self.__dict__.get("_ref")
+        key = tuple(self.__dict__.values())
+        r = self._refs.get(key)
         if r is None:
-            r = self.__dict__["_ref"] = ctypes.byref(self.c())
+            if len(self._refs) >= 256:
+                self._refs.clear()
+            r = self._refs[key] = ctypes.byref(self.c())
         return r
-
-    def __getstate__(self):
-        return {k: v for k, v in self.__dict__.items() if k != "_ref"}
 
 
 @dataclasses.dataclass

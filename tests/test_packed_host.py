@@ -246,7 +246,7 @@ def test_binding_refuses_mixed_dtypes():
 
 
 def test_params_struct_follows_the_fields():
-    """The C struct of a Params is kept between calls and made anew after a change."""
+    """Equal fields share one C struct; a changed field is another one."""
     import copy
     import dataclasses
     import pickle
@@ -257,10 +257,14 @@ def test_params_struct_follows_the_fields():
     p.topk, p.n_hist_chunks = 7, 9
     assert struct(p).topk == 7 and struct(p).hist_head_stride == 9 * 64
     for q in (other, again, copy.deepcopy(other), dataclasses.replace(other)):
-        assert q == hga.Params(**ATTN) and struct(q).topk == 4
+        assert q == hga.Params(**ATTN) and struct(q).topk == 4 and struct(q).n_hist_chunks == 8
     setattr(other, "qblock_end", 2)
-    assert struct(other).qblock_end == 2
+    assert struct(other).qblock_end == 2 and struct(again).qblock_end == 0
     q = _proj()
     assert struct(q).seq_len == 5
     q.seq_len = 6
     assert struct(q).seq_len == 6 and struct(q).kv_head_stride == 6
+    for n in range(1000):  # many shapes: the store of structs stays small
+        p.n_hist_chunks = n
+        assert struct(p).n_hist_chunks == n
+    assert len(hga.Params._refs) <= 256
