@@ -18,10 +18,11 @@
 // flight; K's extremes and sums cross threads through shared memory, V's stay in the lanes
 // of a row, and V's codes are turned there from token to channel order.  Choosing 16,384
 // codes a chunk costs more issue time (0.61 of the slots) than its bytes cost bandwidth, so
-// the choice is made of two-element FMAs and one multiply-add into the word: 22.6 us for
-// 1,792 bf16 chunks of D = 128 (75 MB: 11.5 us at the measured copy rate) against 56 us with
-// a rounding, a conversion and a 64-bit decision of the border cases per element; K and V in
-// CTAs of their own, at twice the CTAs, took 10 us more.
+// the choice is made of two-element FMAs and one multiply-add into the word.  1,792 bf16
+// chunks of D = 128 packed and unpacked take 30.0 us (150 MB: 23 us at the measured copy
+// rate), 65 us when each element took a rounding, a conversion and, near a border, a 64-bit
+// decision.  Four CTAs an SM (64 registers) against three: 30.0 and 31.3 us; K and V in CTAs
+// of their own: 41.5 us.
 #include <cfloat>
 
 #include "dependent.cuh"
@@ -202,7 +203,7 @@ template <typename T> __device__ __forceinline__ uint32_t word_max(uint32_t a, u
 // Thread (col, slot) owns VEC channels of the rows slot, slot + NSLOT, ...: the split of
 // summaries_kernel, whose sums are repeated here in the same order bit for bit.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
     pack_kernel(const T *__restrict__ k, const T *__restrict__ v, long long head_stride, int n_chunks, int first_chunk,
                 uint8_t *__restrict__ hist, long long cap, float *__restrict__ summ, long long summ_cap) {
     using P = Packed<D>;
