@@ -63,6 +63,41 @@ __device__ __forceinline__ Grid grid_of(uint32_t b) {
 // 1 / (15 s) to within 2^-21, 0 for s = 0 (every element is code 0).
 __device__ __forceinline__ float grid_inv(float s) { return s == 0.f ? 0.f : __fdividef(1.f / 15.f, s); }
 
+// An element is decided again when it lies further than this many steps from the value of its
+// approximated code (r of codes() below).  fp32 can tell, for most grids; in units of s, with
+// s taken as 1 .. 2:
+//   * (16 + c) s and borders have 14 significant bits, the last at 2^-8, and their sum with z is
+//     exact for 2^-10 s <= |z| <= 2^14 s and for z = 0.  Grids of bf16 elements keep to that: a range is
+//     no less than the last place of an extreme, and a z this small the difference of two
+//     8-bit numbers.
+//   * r is then rounded only if x is small beside s and a border lies next to x: fp32 elements
+//     so near to a border, ties among them, count as further.  The only border as near to
+//     a bf16 element without being equal to it (2^-14 s, twice what codes() rounds to a tie) is 0:
+//     grids that have it are looked through for such elements (ties, 0.2% of Gaussian elements,
+//     are too many to be decided again).
+//   * x - z and 1 / (15 s) are normal numbers up to s = 2^120.
+// odd_grid() names the others, and the bf16 grids with the border 0 (one Gaussian group in 600).
+template <typename T> constexpr float kReach = sizeof(T) == 4 ? 0.5f - 0x1p-23f : 0.5f;
+template <typename T> __device__ __forceinline__ bool odd_grid(const Grid &g, float inv) {
+    if constexpr (sizeof(T) == 4) {
+        const float z = fabsf(g.z);
+        return g.s > 0x1p120f || (g.s != 0.f && (z > 0x1p14f * g.s || (z != 0.f && z < 0x1p-10f * g.s)));
+    } else {
+        const float m = rintf(fmaf(-15.f * inv, g.z, -0.5f)) + 0.5f;  // the border next to 0
+        return g.s > 0x1p120f || (g.s != 0.f && fmaf(m, g.s, g.z) == 0.f);
+    }
+}
+// While codes are chosen, the step of such a grid has its sign bit set: every r, meaningless
+// then, is further than a negative number, without a comparison more on the common path.
+constexpr uint32_t kOdd = 0x8000u;
+// Whether an element of a grid with step s (as marked) is decided again, its r being further.
+template <typename T> __device__ __forceinline__ bool again(float x, float s) {
+    return sizeof(T) == 4 || !(s < 0.f) || s < -0x1p120f || (x != 0.f && fabsf(x) < -0x1p-14f * s);
+}
+template <typename T> __device__ __forceinline__ uint32_t mark_odd(uint32_t grid, float inv) {
+    return odd_grid<T>(grid_of(grid), inv) ? grid | kOdd : grid;
+}
+
 __device__ __forceinline__ float min_nan(float a, float b) {
     float r;
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
@@ -83,10 +118,8 @@ template <bool kNibble> __device__ constexpr int code_shift(int e) {
 // [0, 1] and 15 p is within 2^-17 of the quotient.  Rounding it to 2^-14 turns what lies that
 // close to a border into a tie, which the rounding to an integer (adding 1.5 2^23 leaves the
 // integer in the low bits) gives to the even code.  A true tie belongs there; an element
-// that does not is more than half a step from its code, and r = x - ((16 + c) s + z) tells:
-// the sum is exact (14 bits of the product against 8 of z) unless z is beyond 2^16 s or,
-// other than zero, below 2^-12 s, and so is the difference of two numbers this close.  r[e]
-// is for the caller to compare with s / 2.
+// that does not is more than half a step from its code, and r = x - ((16 + c) s + z) tells.
+// r[e] is for the caller to compare with kReach s.
 template <int N, bool kNibble>
 __device__ __forceinline__ uint32_t codes(const float (&x)[N], const float (&ss)[N], const float (&zs)[N],
                                           const float (&inv)[N], float (&r)[N]) {
@@ -113,10 +146,10 @@ __device__ __forceinline__ uint32_t codes(const float (&x)[N], const float (&ss)
     return w - off;
 }
 
-// A code, at most one off, decided by its borders (16 + k +- 1/2) s + z.
-__device__ __forceinline__ uint32_t exact_code(float x, const Grid &g, uint32_t k) {
+// A code, at most one off, decided by its borders (16 + k +- 1/2) s + z, which fp32 holds.
+__device__ __forceinline__ uint32_t border_code(float x, const Grid &g, uint32_t k) {
     const float up = fmaf(16.5f + (float)k, g.s, g.z), dn = fmaf(15.5f + (float)k, g.s, g.z);
-    const bool odd = k & 1;
+    const bool odd = k & 1;  // a tie leaves an odd code
     if (x > up || (x == up && odd))
         k = k < 15u ? k + 1u : k;
     else if (x < dn || (x == dn && odd))
@@ -125,28 +158,52 @@ __device__ __forceinline__ uint32_t exact_code(float x, const Grid &g, uint32_t 
     return g.s == 0.f ? 0u : k;
 }
 
-// A word's codes decided again: four elements of one grid staged as bytes, or the 16 bytes
-// of elements (8 or 4) with a grid each as nibbles.  Few warps come here: one element in 2^15
-// of arbitrary ones, and groups whose z lost more than half a step to its rounding; calls,
-// so that the common path holds neither their code nor their registers.
+// The code of any grid with s > 0: x - z as the sum of its rounding y and what that lost, against
+// the borders (q +- 1/2) s.  Rounding is monotonic, so y on one side of a border has x - z there
+// too, and y on it leaves the decision to the rest.  Above s = 2^120 all three are scaled, so that
+// x - z does not overflow.
+__device__ __forceinline__ uint32_t exact_code(float x, const Grid &g) {
+    const float f = g.s > 0x1p120f ? 0.0625f : 1.f, v = x * f, z = g.z * f, s = g.s * f;
+    const float y = __fsub_rn(v, z), vr = __fadd_rn(y, z);
+    const float rest = __fadd_rn(__fsub_rn(v, vr), __fsub_rn(__fsub_rn(vr, y), z));
+    // within 2^-18 of the quotient: at most one border off
+    int q = __float2int_rn(fminf(fmaxf(__fdividef(y, s), 16.f), 31.f));
+    const float up = ((float)q + 0.5f) * s, dn = ((float)q - 0.5f) * s;
+    const bool odd = q & 1;
+    if (q < 31 && (y > up || (y == up && (odd ? rest >= 0.f : rest > 0.f))))
+        ++q;
+    else if (q > 16 && (y < dn || (y == dn && (odd ? rest <= 0.f : rest < 0.f))))
+        --q;
+    return (uint32_t)q - 16u;
+}
+
+__device__ __forceinline__ uint32_t decide(float x, uint32_t grid, uint32_t k) {
+    const Grid g = grid_of(grid & ~kOdd);
+    return grid & kOdd ? exact_code(x, g) : border_code(x, g, k);
+}
+
+// A word's codes decided again: four elements of one grid staged as bytes, or those of the 16
+// bytes of elements (8 or 4) with a grid each that `which` names, as nibbles.  Few warps come
+// here: one element in 2^15 of arbitrary ones, odd grids, and groups whose z lost more than half
+// a step to its rounding; calls, so that the common path holds neither their code nor their
+// registers (a call costs a warp 1 to 3 us).
 __device__ __noinline__ uint32_t exact_bytes(float x0, float x1, float x2, float x3, uint32_t grid, uint32_t word) {
-    const Grid g = grid_of(grid);
-    return exact_code(x0, g, word & 15u) | exact_code(x1, g, word >> 8 & 15u) << 8 |
-           exact_code(x2, g, word >> 16 & 15u) << 16 | exact_code(x3, g, word >> 24 & 15u) << 24;
+    return decide(x0, grid, word & 15u) | decide(x1, grid, word >> 8 & 15u) << 8 |
+           decide(x2, grid, word >> 16 & 15u) << 16 | decide(x3, grid, word >> 24 & 15u) << 24;
 }
 template <typename T>
-__device__ __noinline__ uint32_t exact_nibbles(uint4 x, const uint32_t *grids, uint32_t word) {
+__device__ __noinline__ uint32_t exact_nibbles(uint4 x, const uint32_t *grids, uint32_t word, uint32_t which) {
     constexpr int N = Vec16<T>::N;
     const uint32_t raw[4] = {x.x, x.y, x.z, x.w};
-    uint32_t w = 0;
 #pragma unroll
     for (int e = 0; e < N; ++e) {
+        if (!(which >> e & 1u)) continue;
         const int sh = code_shift<true>(e);
         const uint32_t bf = raw[e / 2 % 4];  // bf16: the word that holds element e
         const float f = __uint_as_float(N == 4 ? raw[e % 4] : (e & 1 ? bf & 0xFFFF0000u : bf << 16));
-        w |= exact_code(f, grid_of(grids[e]), word >> sh & 15u) << sh;
+        word = (word & ~(15u << sh)) | decide(f, grids[e], word >> sh & 15u) << sh;
     }
-    return w;
+    return word;
 }
 
 // Extremes of elements, NaN if one is NaN.  For bf16 the word (-min, max) of a pair of
@@ -303,9 +360,10 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
             vs[D + at] = (uint16_t)(bits >> 16);
         }
         const int lane0 = (tid & 31) & ~(GL - 1);
+        const uint32_t marked = mark_odd<T>(bits, own_inv);
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
-            vgrid[r] = __shfl_sync(0xffffffffu, bits, lane0 + PER * r);
+            vgrid[r] = __shfl_sync(0xffffffffu, marked, lane0 + PER * r);
             vinv[r] = __shfl_sync(0xffffffffu, own_inv, lane0 + PER * r);
         }
     }
@@ -329,7 +387,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
             const float (&i4)[4] = reinterpret_cast<const float (&)[4]>(iv[e]);
             float d[4];
             uint32_t w = codes<4, false>(x4, s4, z4, i4, d);
-            if (fmaxf(fmaxf(fabsf(d[0]), fabsf(d[1])), fmaxf(fabsf(d[2]), fabsf(d[3]))) > 0.5f * g.s)
+            if (fmaxf(fmaxf(fabsf(d[0]), fabsf(d[1])), fmaxf(fabsf(d[2]), fabsf(d[3]))) > kReach<T> * g.s &&
+                (again<T>(x4[0], g.s) || again<T>(x4[1], g.s) || again<T>(x4[2], g.s) || again<T>(x4[3], g.s)))
                 w = exact_bytes(x4[0], x4[1], x4[2], x4[3], vgrid[r], w);
             *reinterpret_cast<uint32_t *>(vcodes + (slot + r * NSLOT) * CS + col + e) = w;
         }
@@ -353,14 +412,15 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
             const uint32_t g0 = grid_bits(make_grid(__uint_as_float(mn << 16), __uint_as_float(mx << 16)));
             const uint32_t g1 =
                 grid_bits(make_grid(__uint_as_float(mn & 0xFFFF0000u), __uint_as_float(mx & 0xFFFF0000u)));
-            *reinterpret_cast<uint2 *>(&kgrid[2 * w]) = make_uint2(g0, g1);
-            *reinterpret_cast<float2 *>(&kinv[2 * w]) = make_float2(grid_inv(grid_of(g0).s), grid_inv(grid_of(g1).s));
+            const float i0 = grid_inv(grid_of(g0).s), i1 = grid_inv(grid_of(g1).s);
+            *reinterpret_cast<uint2 *>(&kgrid[2 * w]) = make_uint2(mark_odd<T>(g0, i0), mark_odd<T>(g1, i1));
+            *reinterpret_cast<float2 *>(&kinv[2 * w]) = make_float2(i0, i1);
             *reinterpret_cast<uint32_t *>(gs + 2 * w) = __byte_perm(g0, g1, 0x5410);
             *reinterpret_cast<uint32_t *>(gs + D + 2 * w) = __byte_perm(g0, g1, 0x7632);
         } else {
             const uint32_t g = grid_bits(make_grid(__uint_as_float(mn), __uint_as_float(mx)));
-            kgrid[w] = g;
             kinv[w] = grid_inv(grid_of(g).s);
+            kgrid[w] = mark_odd<T>(g, kinv[w]);
             gs[w] = (uint16_t)g;
             gs[D + w] = (uint16_t)(g >> 16);
         }
@@ -410,10 +470,31 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
     }
     bool redo = false;
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) redo |= far[e] > 0.5f * ss[e];
+    for (int e = 0; e < VEC; ++e) redo |= far[e] > kReach<T> * ss[e];
     if (redo) {
+        uint32_t which = 0;
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r) kw[r] = exact_nibbles<T>(xr[r], &kgrid[col], kw[r]);
+        for (int e = 0; e < VEC; ++e) which |= (far[e] > kReach<T> * ss[e] ? 1u : 0u) << e;
+        if constexpr (sizeof(T) == 2) {
+            uint32_t left = which;  // almost always one channel, and an odd one
+#pragma unroll 1
+            while (left) {
+                const int e = __ffs(left) - 1;
+                left &= left - 1u;
+                const float s = grid_of(kgrid[col + e]).s;
+                bool any = false;
+#pragma unroll
+                for (int r = 0; r < ROWS; ++r) {
+                    const uint32_t w = e < 4 ? (e < 2 ? xr[r].x : xr[r].y) : (e < 6 ? xr[r].z : xr[r].w);
+                    any |= again<T>(__uint_as_float(e & 1 ? w & 0xFFFF0000u : w << 16), s);
+                }
+                if (!any) which ^= 1u << e;
+            }
+        }
+        if (which) {
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) kw[r] = exact_nibbles<T>(xr[r], &kgrid[col], kw[r], which);
+        }
     }
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {

@@ -161,6 +161,73 @@ def test_values_next_to_the_borders_between_codes(offset):
     assert np.array_equal(hist.cpu().numpy(), ref.pack(f64(k), f64(v))[0])
 
 
+# Groups of 64 elements whose distances x - z, or (16 + c) s + z, do not fit 24 bits; every grid
+# below is exactly representable, so that borders fall where they are meant to.
+def _huge_ranges(rng, n):
+    """Finite grids of which x - z, up to 31 s, passes the largest fp32 number."""
+    lo = np.array([0.0, 1e37, 1e38, -1e38, -3e37])[rng.integers(0, 5, n)][:, None]
+    hi = lo + 10.0 ** rng.uniform(36, 38.3, n)[:, None]
+    x = np.linspace(lo[:, 0], np.minimum(hi, 3.3e38)[:, 0], 64, axis=1)
+    x[n // 2:] = lo[n // 2:] + rng.random((n - n // 2, 64)) * (np.minimum(hi, 3.3e38) - lo)[n // 2:]
+    x[:, 0] = lo[:, 0]
+    return x
+
+
+def _far_offsets(rng, n):
+    """Steps of 8 bits at offsets of 2^12 to 2^23 steps: elements at, and a few places beside, the borders."""
+    step = rng.integers(128, 256, n)[:, None] / 128.0
+    x = 2.0 ** rng.integers(12, 24, n)[:, None] + 16 * step + rng.integers(0, 31, (n, 64)) / 2 * step
+    x = _beside(rng, x, 2)
+    x[:, :2] = x[:, :1] + np.array([0, 15]) * step
+    return x
+
+
+def _small_z(rng, n):
+    """Smallest elements a few places of fp32 from 16 steps: z is 2^-19 to 2^-16 of the step."""
+    step = rng.integers(128, 256, n)[:, None] / 128.0
+    lo = 16 * step * (1 + rng.integers(-8, 9, n)[:, None] * 2.0 ** -23)
+    x = np.maximum(_beside(rng, 16 * step + rng.integers(0, 31, (n, 64)) / 2 * step, 2), lo)
+    x[:, :2] = lo + np.array([0, 15]) * step
+    return x
+
+
+def _border_at_zero(rng, n):
+    """Grids with the border between two codes at 0, or 2^-8 of a step from it, and elements closer still."""
+    step, m = rng.integers(128, 256, n)[:, None] / 128.0, rng.integers(0, 15, n)[:, None]
+    z = -(m + 16.5) * step
+    ok = (ref.to_bf16(z) == z) | (rng.random((n, 1)) < 0.3)
+    x = rng.choice([-1, 1], (n, 64)) * 2.0 ** rng.integers(-38, -9, (n, 64)) * step + (rng.random((n, 1)) < 0.5) * 2.0 ** -8 * step
+    x[:, 2:12] = (rng.integers(0, 31, (n, 10)) / 2 - m - 0.5) * step
+    x[:, :2] = (np.array([0, 15]) - m - 0.5) * step
+    return np.where(ok, x, rng.standard_normal((n, 64)))
+
+
+def _beside(rng, x, places):
+    """fp32 values up to so many places beside x."""
+    x = np.asarray(x, np.float32)
+    return (x.view(np.int32) + rng.integers(-places, places + 1, x.shape).astype(np.int32)).view(np.float32).astype(np.float64)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("groups", [_huge_ranges, _far_offsets, _small_z, _border_at_zero], ids=lambda f: f.__name__[1:])
+def test_codes_where_fp32_distances_round(groups, dtype):
+    """The nearest code of every finite group: record for record the 64-bit decision."""
+    import hierarchical_sparse_long_b200 as hga
+    dt = BF16 if dtype == "bf16" else torch.float32
+    rng = np.random.default_rng(17)
+    D, n = 128, 24
+    x = groups(rng, 2 * n * D)
+    k = host(x[:n * D].reshape(n, D, 64).swapaxes(1, 2).reshape(1, 1, n * 64, D), dt)  # a channel of a chunk is a group
+    v = host(x[n * D:].reshape(n, 2, 64, 64).swapaxes(1, 2).reshape(1, 1, n * 64, D), dt)  # 64 channels of a token
+    hist = torch.zeros(1, 1, n, 72 * D, device="cuda", dtype=torch.uint8)
+    hga.hga_pack_history(k, v, n * 64, 1, 1, D, 0, n, hist, n)
+    want, kv, vv = ref.pack(f64(k), f64(v))
+    got = hist.cpu().numpy()
+    assert np.isfinite(kv).any(axis=2).mean() > 0.5  # not all of the grids overflow
+    bad = np.argwhere(got != want)
+    assert not len(bad), f"{len(bad)} of {want.size} bytes differ, the first at {bad[0]}"
+
+
 # ------------------------------------------------------------------ attention
 class Packed:
     """A packed history of random chunks, its values in 64 bits and a bf16 window or segment."""
