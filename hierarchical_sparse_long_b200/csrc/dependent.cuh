@@ -2,7 +2,9 @@
 // kernel drains: a launch of its own costs about 2 us between two kernels, as much as the
 // smallest of them run.  A kernel launched this way calls depend_wait() in every CTA before
 // its first access of global memory: it returns once the previous kernel has completed and
-// its writes are visible, so nothing that an earlier kernel still uses is touched.  The
+// its writes are visible, so nothing that an earlier kernel still uses is touched.  Its pointers
+// are not __restrict__: that would promise that nobody else writes what the kernel reads while
+// it lives, and let the compiler move those loads above the wait.  The
 // kernel behind it may take its place the same way once every CTA of this one has called
 // depend_next() or ended.  That call stands near a CTA's end: CTAs that come to wait among
 // running ones fill the SMs unevenly (at the start of the decode kernel it cost 3 of 14 us).

@@ -641,3 +641,57 @@ def test_calls_behind_one_another(mode):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(seen, want))
     del graph
+
+
+@pytest.mark.parametrize("mode", ["stream", "graph"])
+def test_calls_behind_another_streams_event(mode):
+    """A call behind an event reads what the event's stream wrote just before it, and a call of that
+    stream behind an event of this one writes only what this one has read: projection on one
+    stream, records, their values and decode on the other, into the same buffers again and again."""
+    import hierarchical_sparse_long_b200 as hga
+    B, Hq, Hkv, D, steps, n = 2, 8, 2, 128, 6, 256
+    rng = np.random.default_rng(41)
+    row = (Hq + 2 * Hkv) * D
+    x = host(rng.standard_normal((steps, B, n, row)))
+    w = host(1 + 0.1 * rng.standard_normal(D))
+    table = torch.empty(n, D, device="cuda")
+    hga.hga_rope_table(1e6, D, n, table)
+    buf = lambda *s, t=BF16: torch.zeros(*s, device="cuda", dtype=t)
+    q, k, v = buf(B, Hq, n, D), buf(B, Hkv, n, D), buf(B, Hkv, n, D)
+    k2, v2, hist = buf(steps, B, Hkv, n, D), buf(steps, B, Hkv, n, D), buf(B, Hkv, n // 64, 72 * D, t=torch.uint8)
+    q1, idx = buf(B, Hq, 1, D) + 1, torch.arange(n // 64, device="cuda", dtype=torch.int32).expand(B, Hkv, 1, -1).contiguous()
+    out, lse = buf(steps, B, Hq, 1, D), buf(steps, B, Hq, 1, t=torch.float32)
+    p = hga.ProjParams(B, Hq, Hkv, D, n, D)
+    d = hga.Params(B, Hq, Hkv, D, n // 64, 1, n // 64, seg_head_stride=n, q_block=1)
+    side = torch.cuda.Stream()
+
+    def run(idle):
+        main = torch.cuda.current_stream()
+        for i in range(steps):
+            side.wait_stream(main)
+            a = x[i]
+            hga.hga_qk_norm_rope(p, a, a[..., Hq * D:], a[..., (Hq + Hkv) * D:], w, w, table, None, q, k, v, side)
+            main.wait_stream(side)
+            if idle:
+                torch.cuda.synchronize()
+            hga.hga_pack_history(k, v, n, B, Hkv, D, 0, n // 64, hist, n // 64)
+            hga.hga_unpack_history(hist, n // 64, B, Hkv, D, 0, n // 64, k2[i], v2[i], n)
+            hga.hga_attn_decode_packed(d, q1, hist, n // 64, k, v, n, idx, out[i], lse[i])
+            if idle:
+                torch.cuda.synchronize()
+
+    run(True)
+    want = [t.clone() for t in (k2, v2, out, lse)]
+    assert all(torch.isfinite(t).all() for t in want)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    if mode == "graph":
+        with torch.cuda.graph(graph):
+            run(False)
+    for _ in range(10):
+        for t in (q, k, v, k2, v2, hist, out, lse):
+            t.zero_()
+        graph.replay() if mode == "graph" else run(False)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((k2, v2, out, lse), want))
+    del graph

@@ -268,3 +268,17 @@ def test_params_struct_follows_the_fields():
         p.n_hist_chunks = n
         assert struct(p).n_hist_chunks == n
     assert len(hga.Params._refs) <= 256
+
+
+def test_dependent_kernels_promise_nothing_about_aliasing():
+    """A kernel that takes its place before the previous one has ended must not tell the compiler
+    that its inputs are constant: loads of const __restrict__ pointers may pass the wait."""
+    import os
+    from hierarchical_sparse_long_b200 import build
+    waiting = 0
+    for path in build.sources():
+        text = open(path).read()
+        if "depend_wait()" in text or "griddepcontrol.wait" in text:
+            waiting += 1
+            assert "__restrict__" not in text and "__ldg" not in text, os.path.basename(path)
+    assert waiting >= 4
