@@ -244,6 +244,34 @@ def dtype_code(t) -> int:
     raise HGAError(-1, "unsupported tensor dtype", str(t.dtype))
 
 
+class _Types:
+    """The types of a call's tensors, whose memory is read, or written, as those: by the letters
+    e (the call's element type), f (fp32) and i (int32), a tuple to compare with in one go."""
+
+    def __init__(self, letters: str):
+        self.letters, self.of = letters, {}
+
+    def _make(self, code: int):
+        import torch
+        of = {"e": {HGA_BF16: torch.bfloat16, HGA_FP32: torch.float32}.get(code), "f": torch.float32, "i": torch.int32}
+        self.of[code] = tuple(of[c] for c in self.letters)
+        return self.of[code]
+
+    def want(self, code: int) -> tuple:
+        return self.of.get(code) or self._make(code)
+
+    def refuse(self, what: str, code: int, names: str, *tensors):
+        """Raises for the first tensor of another type; a missing one, and a code that is none, are
+        the library's to refuse."""
+        for name, t, want in zip(names.split(), tensors, self.want(code)):
+            if t is not None and want is not None and t.dtype != want:
+                raise HGAError(-1, what, f"{name} of {t.dtype}, not {want}")
+
+
+_FWD_TYPES, _BWD_TYPES, _ATTN_TYPES = _Types("eeeeeeee"), _Types("eeeeeeefffff"), _Types("eeeeif")
+_F32, _INT32 = _Types("f"), _Types("i")
+
+
 def hga_build_summaries(k, head_stride: int, batch: int, n_kv_heads: int, head_dim: int, chunk: int,
                         first_chunk: int, n_chunks: int, summ, summ_cap_chunks: int, stream=None):
     """Chunk summaries (mean of keys) for chunks [first_chunk, first_chunk + n_chunks)."""
@@ -497,18 +525,46 @@ def hga_selftest_wait_timeout(wait_cycles: int, stream=None):
 
 def hga_rope_table(theta: float, rotary_dim: int, n_pos: int, table, stream=None):
     """cos / sin rows of positions [0, n_pos) into table [n_pos][rotary_dim] (fp32)."""
+    _F32.refuse("hga_rope_table", HGA_FP32, "table", table)
+    if table is not None and (table.numel() < n_pos * rotary_dim or not table.is_contiguous()):
+        raise HGAError(-1, "hga_rope_table", f"table of {tuple(table.shape)}, not [{n_pos}][{rotary_dim}] in one piece")
     _check(lib().hga_rope_table(theta, rotary_dim, n_pos, _ptr(table), _stream(stream)), "hga_rope_table")
 
 
-def _table_rows(p: ProjParams, table) -> int:
-    return 0 if table is None or p.rotary_dim == 0 else table.numel() // p.rotary_dim
+def _table_rows(what: str, p: ProjParams, table, positions) -> int:
+    """Positions that the table holds; refuses a table or positions of another type or layout."""
+    if positions is not None:
+        if positions.dtype != _INT32.want(HGA_BF16)[0]:
+            _INT32.refuse(what, HGA_BF16, "positions", positions)
+        if positions.numel() != p.batch * p.seq_len or not positions.is_contiguous():
+            raise HGAError(-1, what,
+                           f"positions of {tuple(positions.shape)}, not [{p.batch}][{p.seq_len}] in one piece")
+    r = p.rotary_dim
+    if table is None or r <= 0:
+        return 0
+    if table.dtype != _F32.want(HGA_FP32)[0]:
+        _F32.refuse(what, HGA_FP32, "table", table)
+    n = table.numel()
+    # whole rows of r next to one another
+    if n % r or (table.stride() != (r, 1) and not (table.is_contiguous() and
+                                                   (table.dim() < 2 or table.shape[-1] == r))):
+        raise HGAError(-1, what, f"table of {tuple(table.shape)}, not [positions][{r}] in one piece")
+    return n // r
 
 
 def hga_qk_norm_rope(p: ProjParams, q, k, v, q_weight, k_weight, table, positions, q_out, k_out, v_out, stream=None):
     """Per-head norm of q and k, position rotation and head-major layout of q, k and v from a
     layer's projections; positions int32 [B][S] (-1: padding row) or None for p.first_pos + i."""
+    try:
+        types = (q.dtype, k.dtype, v.dtype, q_weight.dtype, k_weight.dtype, q_out.dtype, k_out.dtype, v_out.dtype)
+    except AttributeError:  # a missing tensor
+        types = None
+    if types != _FWD_TYPES.want(p.dtype):
+        _FWD_TYPES.refuse("hga_qk_norm_rope", p.dtype, "q k v q_weight k_weight q_out k_out v_out", q, k, v, q_weight,
+                          k_weight, q_out, k_out, v_out)
+    n_pos = _table_rows("hga_qk_norm_rope", p, table, positions)
     _check(lib().hga_qk_norm_rope(p.ref(), _ptr(q), _ptr(k), _ptr(v), _ptr(q_weight), _ptr(k_weight),
-                                  _ptr(table), _table_rows(p, table), _ptr(positions), _ptr(q_out), _ptr(k_out),
+                                  _ptr(table), n_pos, _ptr(positions), _ptr(q_out), _ptr(k_out),
                                   _ptr(v_out), _stream(stream)), "hga_qk_norm_rope")
 
 
@@ -520,9 +576,19 @@ def hga_qk_norm_rope_bwd(p: ProjParams, q, k, q_weight, k_weight, table, positio
                          dq_weight, dk_weight, workspace, stream=None):
     """Backward of hga_qk_norm_rope: gradients of the projections (dtype) and of the weights (fp32)
     from the attention's fp32 dq, dk, dv."""
+    try:
+        types = (q.dtype, k.dtype, q_weight.dtype, k_weight.dtype, dq_in.dtype, dk_in.dtype, dv_in.dtype, dq.dtype,
+                 dk.dtype, dv.dtype, dq_weight.dtype, dk_weight.dtype)
+    except AttributeError:
+        types = None
+    if types != _BWD_TYPES.want(p.dtype):
+        _BWD_TYPES.refuse("hga_qk_norm_rope_bwd", p.dtype,
+                          "q k q_weight k_weight dq_in dk_in dv_in dq dk dv dq_weight dk_weight", q, k, q_weight,
+                          k_weight, dq_in, dk_in, dv_in, dq, dk, dv, dq_weight, dk_weight)
+    n_pos = _table_rows("hga_qk_norm_rope_bwd", p, table, positions)
     nbytes = workspace.numel() * workspace.element_size()
     _check(lib().hga_qk_norm_rope_bwd(p.ref(), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight),
-                                      _ptr(table), _table_rows(p, table), _ptr(positions), _ptr(dq), _ptr(dk),
+                                      _ptr(table), n_pos, _ptr(positions), _ptr(dq), _ptr(dk),
                                       _ptr(dv), _ptr(dq_in), _ptr(dk_in), _ptr(dv_in), _ptr(dq_weight),
                                       _ptr(dk_weight), _ptr(workspace), nbytes, _stream(stream)),
            "hga_qk_norm_rope_bwd")
@@ -543,6 +609,8 @@ def hga_pack_history(k, v, head_stride: int, batch: int, n_kv_heads: int, head_d
                      n_chunks: int, hist, hist_cap_chunks: int, summ=None, summ_cap_chunks: int = 0, stream=None):
     """Packs closed chunks (rows 0 .. of k / v) into the 4-bit records [first_chunk, first_chunk +
     n_chunks) of hist, and appends their summaries when summ is given."""
+    if summ is not None and summ.dtype != _F32.want(HGA_FP32)[0]:
+        _F32.refuse("hga_pack_history", HGA_FP32, "summ", summ)
     _check(lib().hga_pack_history(_ptr(k), _ptr(v), head_stride, batch, n_kv_heads, head_dim, first_chunk, n_chunks,
                                   _kv_dtype(k, v), _ptr(hist), hist_cap_chunks, _ptr(summ), summ_cap_chunks,
                                   _stream(stream)), "hga_pack_history")
@@ -556,8 +624,18 @@ def hga_unpack_history(hist, hist_cap_chunks: int, batch: int, n_kv_heads: int, 
            "hga_unpack_history")
 
 
+def _attn_types(what: str, p: Params, q, k, v, idx, out, lse):
+    try:
+        types = (q.dtype, k.dtype, v.dtype, out.dtype, idx.dtype, lse.dtype)
+    except AttributeError:
+        types = None
+    if types != _ATTN_TYPES.want(p.dtype):
+        _ATTN_TYPES.refuse(what, p.dtype, "q k v out idx lse", q, k, v, out, idx, lse)
+
+
 def hga_attn_fwd_packed(p: Params, q, hist, hist_cap_chunks: int, k_seg, v_seg, idx, out, lse, stream=None):
     """hga_attn_fwd over a packed (4-bit) history."""
+    _attn_types("hga_attn_fwd_packed", p, q, k_seg, v_seg, idx, out, lse)
     _check(lib().hga_attn_fwd_packed(p.ref(), _ptr(q), _ptr(hist), hist_cap_chunks, _ptr(k_seg),
                                      _ptr(v_seg), _ptr(idx), _ptr(out), _ptr(lse), _stream(stream)),
            "hga_attn_fwd_packed")
@@ -566,6 +644,7 @@ def hga_attn_fwd_packed(p: Params, q, hist, hist_cap_chunks: int, k_seg, v_seg, 
 def hga_attn_decode_packed(p: Params, q, hist, hist_cap_chunks: int, k_local, v_local, n_local: int, idx, out, lse,
                            stream=None):
     """hga_attn_decode over a packed (4-bit) history; the local window is bf16."""
+    _attn_types("hga_attn_decode_packed", p, q, k_local, v_local, idx, out, lse)
     _check(lib().hga_attn_decode_packed(p.ref(), _ptr(q), _ptr(hist), hist_cap_chunks, _ptr(k_local),
                                         _ptr(v_local), n_local, _ptr(idx), _ptr(out), _ptr(lse), _stream(stream)),
            "hga_attn_decode_packed")

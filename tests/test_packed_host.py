@@ -282,3 +282,63 @@ def test_dependent_kernels_promise_nothing_about_aliasing():
             waiting += 1
             assert "__restrict__" not in text and "__ldg" not in text, os.path.basename(path)
     assert waiting >= 4
+
+
+def test_binding_refuses_other_types_and_layouts():
+    """Every tensor is of the type, and tables and positions of the layout, as which the library
+    would read it: anything else gave wrong rows, or rows behind the tensor's end, without an error."""
+    import torch
+    f32, i32, i64, bf = torch.float32, torch.int32, torch.int64, torch.bfloat16
+    B, S, Hq, Hkv, D, R = 2, 5, 4, 2, 64, 32
+    p = hga.ProjParams(B, Hq, Hkv, D, S, R)
+    row = (Hq + 2 * Hkv) * D
+    fwd = dict(q=torch.zeros(B, S, row, dtype=bf), k=torch.zeros(B, S, row, dtype=bf),
+               v=torch.zeros(B, S, row, dtype=bf), q_weight=torch.ones(D, dtype=bf), k_weight=torch.ones(D, dtype=bf),
+               table=torch.zeros(16, R), positions=torch.zeros(B, S, dtype=i32),
+               q_out=torch.zeros(B, Hq, S, D, dtype=bf), k_out=torch.zeros(B, Hkv, S, D, dtype=bf),
+               v_out=torch.zeros(B, Hkv, S, D, dtype=bf))
+    bwd = dict(q=fwd["q"], k=fwd["k"], q_weight=fwd["q_weight"], k_weight=fwd["k_weight"], table=fwd["table"],
+               positions=fwd["positions"], dq=torch.zeros(B, Hq, S, D), dk=torch.zeros(B, Hkv, S, D),
+               dv=torch.zeros(B, Hkv, S, D), dq_in=fwd["q"], dk_in=fwd["q"].clone(), dv_in=fwd["q"].clone(),
+               dq_weight=torch.zeros(D), dk_weight=torch.zeros(D), workspace=torch.zeros(1 << 20, dtype=torch.uint8))
+
+    def refused(call, args, match, **other):
+        with pytest.raises(hga.HGAError, match=match) as e:
+            call(*{**args, **other}.values(), stream=0)
+        assert e.value.code == INVALID
+
+    for call, args in ((lambda *a, **k: hga.hga_qk_norm_rope(p, *a, **k), fwd),
+                       (lambda *a, **k: hga.hga_qk_norm_rope_bwd(p, *a, **k), bwd)):
+        for name, t in args.items():
+            if name == "workspace":
+                continue
+            for dt in {f32, bf, i64} - {t.dtype}:
+                refused(call, args, f"{name} of {dt}", **{name: t.to(dt)})
+        # one row of positions for every sequence, too few, every other one
+        for pos in (torch.arange(S, dtype=i32).expand(B, S), torch.zeros(S, dtype=i32),
+                    torch.zeros(B, 2 * S, dtype=i32)[:, ::2]):
+            refused(call, args, "positions of", positions=pos)
+        # rows of another width, cut from wider ones, half a row
+        for table in (torch.zeros(16, D), torch.zeros(16, D)[:, :R], torch.zeros(16, R // 2), torch.zeros(R + 1)):
+            refused(call, args, "table of", table=table)
+    for table in (torch.zeros(7, R), torch.zeros(16, R)[::2], torch.zeros(8, R, dtype=bf)):
+        with pytest.raises(hga.HGAError, match="table of"):
+            hga.hga_rope_table(1e4, R, 8, table, stream=0)
+    k, hist = torch.zeros(64, D, dtype=bf), torch.zeros(72 * D, dtype=torch.uint8)
+    with pytest.raises(hga.HGAError, match="summ of torch.bfloat16"):
+        hga.hga_pack_history(k, k, 64, 1, 1, D, 0, 1, hist, 1, torch.zeros(D, dtype=bf), 1, stream=0)
+    for decode in (False, True):
+        n = 1 if decode else 64
+        c = hga.Params(1, Hq, Hkv, D, 1, n, 1, q_block=n)
+        q, kv = torch.zeros(1, Hq, n, D, dtype=bf), torch.zeros(1, Hkv, n, D, dtype=bf)
+        args = dict(q=q, hist=hist, cap=1, k=kv, v=kv.clone(), idx=torch.zeros(1, Hkv, 1, 1, dtype=i32),
+                    out=q.clone(), lse=torch.zeros(1, Hq, n))
+
+        def call(q, hist, cap, k, v, idx, out, lse, stream):
+            if decode:
+                hga.hga_attn_decode_packed(c, q, hist, cap, k, v, 1, idx, out, lse, stream=stream)
+            else:
+                hga.hga_attn_fwd_packed(c, q, hist, cap, k, v, idx, out, lse, stream=stream)
+        for name in ("q", "k", "v", "idx", "out", "lse"):
+            for dt in {f32, bf, i64} - {args[name].dtype}:
+                refused(call, args, f" of {dt}", **{name: args[name].to(dt)})
