@@ -60,12 +60,19 @@ class _Mirror:
         cls._refs = {}
 
     def ref(self):
-        key = tuple(self.__dict__.values())
-        r = self._refs.get(key)
+        fields = self.__dict__
+        key = (*fields, *fields.values())  # names too: another order of fields is another key
+        try:
+            r = self._refs.get(key)
+        except TypeError:  # not hashable
+            return ctypes.byref(self.c())
         if r is None:
-            if len(self._refs) >= 256:
-                self._refs.clear()
-            r = self._refs[key] = ctypes.byref(self.c())
+            r = ctypes.byref(self.c())
+            # a number that can change in place (a tensor is hashed by identity) has no lasting struct
+            if all(type(v) in (int, float, bool) for v in fields.values()):
+                if len(self._refs) >= 256:
+                    self._refs.clear()
+                self._refs[key] = r
         return r
 
 

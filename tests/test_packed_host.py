@@ -342,3 +342,28 @@ def test_binding_refuses_other_types_and_layouts():
         for name in ("q", "k", "v", "idx", "out", "lse"):
             for dt in {f32, bf, i64} - {args[name].dtype}:
                 refused(call, args, f" of {dt}", **{name: args[name].to(dt)})
+
+
+def test_params_struct_of_any_number():
+    """Fields that are not plain numbers, or lie in another order, give the struct of their values."""
+    import torch
+    struct = lambda q: q.ref()._obj
+    n = torch.tensor(4)
+    p = hga.Params(**{**ATTN, "topk": n})
+    assert struct(p).topk == 4
+    n += 3
+    assert struct(p).topk == 7
+    assert struct(hga.Params(**{**ATTN, "topk": np.array(5)})).topk == 5
+    p = hga.Params(**ATTN)
+    p.tag = ["a user's own attribute"]
+    assert struct(p).topk == 4
+    # topk and seg_len have changed places in the instance, and have each other's usual values
+    assert struct(hga.Params(**{**ATTN, "topk": 4, "seg_len": 64})).seg_len == 64
+    swapped = hga.Params.__new__(hga.Params)
+    names = list(hga.Params(**ATTN).__dict__)
+    i, j = names.index("topk"), names.index("seg_len")
+    names[i], names[j] = names[j], names[i]
+    fields = hga.Params(**{**ATTN, "topk": 64, "seg_len": 4}).__dict__
+    for name in names:
+        setattr(swapped, name, fields[name])
+    assert struct(swapped).topk == 64 and struct(swapped).seg_len == 4
