@@ -61,18 +61,18 @@ class _Mirror:
 
     def ref(self):
         fields = self.__dict__
-        key = (*fields, *fields.values())  # names too: another order of fields is another key
+        key = tuple(fields.values())
         try:
-            r = self._refs.get(key)
+            names, r = self._refs.get(key, (None, None))
         except TypeError:  # not hashable
             return ctypes.byref(self.c())
-        if r is None:
-            r = ctypes.byref(self.c())
+        if names != [*fields]:  # not there, or these values in another order of fields
+            names, r = [*fields], ctypes.byref(self.c())
             # a number that can change in place (a tensor is hashed by identity) has no lasting struct
-            if all(type(v) in (int, float, bool) for v in fields.values()):
+            if all(type(v) in (int, float, bool) for v in key):
                 if len(self._refs) >= 256:
                     self._refs.clear()
-                self._refs[key] = r
+                self._refs[key] = names, r
         return r
 
 
