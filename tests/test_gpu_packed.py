@@ -354,6 +354,32 @@ def test_forward(case):
     c.check()
 
 
+# Above two CTAs an SM the blocks run in another order, the shortest first on some SMs; CTAs follow
+# one another on an SM, and its TMEM is released and taken again.
+@pytest.mark.parametrize("case,blocks", [
+    ((2, 32, 8, 128, 3, 9, 20, "random"), None),      # 320 CTAs of two halves
+    ((3, 16, 8, 64, 2, 5, 15, "holes"), None),        # 360 of one
+    ((2, 12, 4, 128, 2, 5, 18, "random"), (2, 17)),   # 360, one head each; the first and the last blocks stay
+    ((2, 32, 8, 64, 2, 0, 21, "random"), (0, 19)),    # 304 of two halves, no history
+], ids=str)
+def test_forward_of_many_blocks(case, blocks):
+    B, Hq, Hkv, D, topk, nc, n, routes = case
+    G = Hq // Hkv
+    c = Packed(B, Hq, Hkv, D, topk, nc, 64 * n, n, routes=routes)
+    if blocks:
+        c.p.qblock_begin, c.p.qblock_end = blocks
+    grid = (blocks[1] - blocks[0] if blocks else n) * B * Hkv * (1 if G % 2 == 0 else G)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert grid >= 2 * sms and grid % sms
+    c.run()
+    c.check(blocks=range(*blocks) if blocks else None)
+    first = c.out.clone(), c.lse.clone()
+    for _ in range(3):  # one behind the other: the next call's CTAs wait beside this one's last
+        c.run()
+    torch.cuda.synchronize()
+    assert torch.equal(c.out, first[0]) and torch.equal(c.lse, first[1])
+
+
 def test_forward_of_a_block_range():
     c = Packed(1, 8, 2, 128, 4, 9, 320, 5)
     c.p.qblock_begin, c.p.qblock_end = 1, 3
