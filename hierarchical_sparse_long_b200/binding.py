@@ -561,7 +561,8 @@ def _table_rows(what: str, p: ProjParams, table, positions) -> int:
 
 def hga_qk_norm_rope(p: ProjParams, q, k, v, q_weight, k_weight, table, positions, q_out, k_out, v_out, stream=None):
     """Per-head norm of q and k, position rotation and head-major layout of q, k and v from a
-    layer's projections; positions int32 [B][S] (-1: padding row) or None for p.first_pos + i."""
+    layer's projections; positions int32 [B][S] (-1: padding row) or None for p.first_pos + i.
+    q, k, v, the weights and the outputs are of p.dtype; table [positions][rotary_dim] fp32."""
     try:
         types = (q.dtype, k.dtype, v.dtype, q_weight.dtype, k_weight.dtype, q_out.dtype, k_out.dtype, v_out.dtype)
     except AttributeError:  # a missing tensor

@@ -36,7 +36,10 @@
 // seconds on end the power cap makes them 80.5 and 291 us.  A 64-token tile of
 // two halves takes about 1,950 cycles, of which its products' operand traffic from shared
 // memory accounts for about 1,470 (a QK product re-reads its 128 rows of queries for 64
-// keys); a half's softmax (about 1,500) and products overlap with the other half's.  128-token
+// keys); a half's softmax (about 1,500) and products overlap with the other half's.  D = 64 takes
+// 66.5 us for the 16K segment (34 GFLOP: 517 TFLOP/s): half the products for the same softmax.
+// Groups that are no multiple of 4 run on one half, an odd head with 64 of its 128 rows spare:
+// 162.6 us for 24 + 8 heads of 128, 187.6 for 28 + 4 (317 and 321 TFLOP/s).  128-token
 // tiles, which re-read the queries half as often, left room for one score buffer per half and
 // took 2,300 cycles per 64 tokens: softmax and products of a half no longer overlap.
 #include "dependent.cuh"
@@ -536,7 +539,9 @@ __global__ void __launch_bounds__(32 * (kIssueWarps + 4 * NH + kProdWarps), 1)
             }
             m_run = m_use;
             // P as bf16 pairs over the first 32 columns of this tile's S buffer (already
-            // read into registers); PV reads it from there as its A operand
+            // read into registers); PV reads it from there as its A operand, and bf16 products
+            // take no wider one: outputs are 2.3e-3 in norm off those of 64 bits, 1.7e-3 with P
+            // in fp32 (their own rounding).  The row sum is of the unrounded P.
             {
                 uint32_t pk[32];
 #pragma unroll
@@ -665,8 +670,10 @@ hga_status_t launch_nh(const hga_params_t &p, const void *q, const uint8_t *hist
     const unsigned grid = (unsigned)(a.n_blocks * n_bg * a.n_sub);
     // An SM runs one CTA at a time, and grid % SMs of the SMs get one more than the others.
     // Longest first alone, those end with a whole short block that nothing else runs beside;
-    // from two CTAs an SM on they take it at the start instead (512 CTAs of the last 128K
-    // segment: 265 -> 254 us; 256 CTAs of the 16K segment: 74.5 -> 76 us, so not there).
+    // from two CTAs an SM on they take it at the start instead.  us without / with, top-16 of 224
+    // chunks: 320 CTAs 109.7 / 96.5, 384 131.6 / 124.0, 448 171.6 / 154.6, 512 202.7 / 186.7, 640
+    // 294.5 / 291.7; top-4 of 64, 384 CTAs 68.9 / 65.0; the last 128K segment (512) 265 / 254.  Below
+    // it gains nothing: 160 CTAs 48.6 / 48.4, 224 66.2 / 66.6, 256 74.5 / 76.
     const unsigned sms = (unsigned)sm_count();
     a.n_first = grid >= 2 * sms ? (int)(grid % sms) : 0;
     return record_cuda(launch_dependent(kern, grid, 32 * (kIssueWarps + 4 * NH + kProdWarps), Smem<D, NH>::ALLOC, 1,

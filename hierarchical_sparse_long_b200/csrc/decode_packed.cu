@@ -27,11 +27,13 @@
 // cluster: one launch, no workspace, sums in a fixed order.
 //
 // Measured: 13.8 us for 16 sequences of 32 + 8 heads at 32 routed chunks and 64 window tokens
-// (42 MB, 3.1 TB/s of the 6.5 that a copy reaches), 4.9 us for one at 16 chunks.  A unit is
-// about 1,040 instructions, half of them shifts and masks of the integer pipe, which two or
-// three warps of a scheduler keep busy; the rest is the start (routes, then first records)
-// and the merge.  With loads into registers in place of the ring, and a merge by CTA and
-// then by cluster, the 16 sequences took 19.6 us.
+// (42 MB, 3.1 TB/s of the 6.5 that a copy reaches), 4.9 us for one at 16 chunks.  No pipe is
+// full there (issue slots 38%, integer pipe 34%, DRAM 30% of their peaks): a unit is a chain of
+// about 1,040 instructions of one warp (1.2 us, 1.9 with two CTAs on the SM), and with 256 CTAs on
+// 148 SMs, some holding one and some two, a scheduler has 1.7 warps to choose from; 36 units over 8
+// warps are five rounds of them.  The rest is the start (routes, then first records) and the
+// merge.  With loads into registers in place of the ring, and a merge by CTA and then by
+// cluster, the 16 sequences took 19.6 us.
 #include <cstddef>
 
 #include "dependent.cuh"
@@ -49,7 +51,7 @@ constexpr int kPiece = 16;      // window tokens per unit
 constexpr int kMaxRouted = 64;  // topk limit of the parameter check
 constexpr int kHeads = 8;       // query heads per KV head: the N side of the products
 constexpr int kMaxCluster = 8;  // portable cluster size
-constexpr int kCtasPerSm = 3;   // 168 registers a thread, 74 KiB of rings a CTA
+constexpr int kCtasPerSm = 3;   // at most 168 registers a thread; 72 KiB of rings a CTA
 constexpr unsigned kSmBytes = 228 * 1024;  // shared memory of an SM
 constexpr int kStages = 2;      // one unit multiplied, one on its way
 
@@ -226,7 +228,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_packed_kernel(con
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[i][e] *= corr[e & 1];
         }
-        // P is rounded to bf16 for the product, as in the other attention kernels
+        // P is rounded to bf16 for the product, as in the other attention kernels: the tensor
+        // cores' bf16 products take no wider P, and the row sum is of the unrounded one.  Outputs
+        // are 2.1e-3 in norm off those of 64 bits, 1.7e-3 with P in fp32 (their own rounding).
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             pt[2 * i] = transpose8(tc::pack_bf16(s[i][0], s[i][1]));
@@ -430,8 +434,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_packed_kernel(con
 // predicts), all resident at once.  With c CTAs on an SM a warp takes about 0.4 + 0.8 c us
 // per unit of D = 128 (1.16 alone, 1.87, 2.75 measured), and a cluster's merge about 0.5 us,
 // 1 us for eight CTAs; the least sum of both is taken.  Measured, us for 1 / 2 / 4 / 8 CTAs:
-//   8 pairs of 19 units    8.5 /  6.8 /  5.8 /  5.4      32 pairs of 20   9.0 /  7.1 /  6.2 /  7.0
-//   128 pairs of 36       15.2 / 14.2 / 20.2 / 27.1     192 pairs of 36  21.5 / 18.5 / 24.1 / 37.3
+//   8 pairs of 19 units    8.1 /  6.3 /  5.1 /  5.0      32 pairs of 19   8.2 /  6.3 /  5.7 /  6.6
+//   128 pairs of 36       14.7 / 13.8 / 20.0 / 26.8     192 pairs of 36  20.9 / 17.8 / 23.7 / 37.0
+// D = 64, whose units are half as long, keeps the order:
+//   8 pairs of 20 units    6.1 /  5.1 /  4.3 /  4.3      32 pairs of 36   9.8 /  6.9 /  5.7 /  6.4
+//   96 pairs of 49        13.2 / 11.1 /  9.7 / 15.9     192 pairs of 49  17.6 / 14.6 / 20.2 / 27.5
 int cluster_size(const hga_params_t &p, int n_local) {
     const long long units =
         (p.topk < p.n_hist_chunks ? p.topk : p.n_hist_chunks) + ((long long)n_local + kPiece - 1) / kPiece;

@@ -17,12 +17,13 @@
 // 0.28 of their bytes written.  One 256-thread CTA takes a chunk, all of its loads in
 // flight; K's extremes and sums cross threads through shared memory, V's stay in the lanes
 // of a row, and V's codes are turned there from token to channel order.  Choosing 16,384
-// codes a chunk costs more issue time (0.61 of the slots) than its bytes cost bandwidth, so
+// codes a chunk costs more issue time (0.68 of the slots) than its bytes cost bandwidth, so
 // the choice is made of two-element FMAs and one multiply-add into the word.  1,792 bf16
-// chunks of D = 128 packed and unpacked take 30.0 us (150 MB: 23 us at the measured copy
-// rate), 65 us when each element took a rounding, a conversion and, near a border, a 64-bit
-// decision.  Four CTAs an SM (64 registers) against three: 30.0 and 31.3 us; K and V in CTAs
-// of their own: 41.5 us.
+// chunks of D = 128 packed and unpacked take 31.9 us (150 MB: 23 us at the measured copy
+// rate); packed alone 20.5 us (75 MB: 11.5), in fp32 30.8 us (135 MB: 20.5).  Both took 65 us
+// when each element took a rounding, a conversion and, near a border, a 64-bit decision, and
+// 30.0 us without the marks of odd grids (below).  Four CTAs an SM (64 registers) against three
+// gained 1.3 us; K and V in CTAs of their own took 41.5 us.
 #include <cfloat>
 
 #include "dependent.cuh"
@@ -526,9 +527,10 @@ __device__ __forceinline__ void load4(const void *p, uint32_t (&r)[4]) {
     r[3] = v.w;
 }
 
-// One CTA per record, bound by the bytes it writes (12.5 us for 1,792 bf16 chunks of
-// D = 128, 75 MB).  K words are 8 channels of a token, one 16-byte store (bf16) each; a V
-// thread turns 8 channels x 8 tokens in registers.
+// One CTA per record, bound by the bytes it writes (13.6 us for 1,792 bf16 chunks of
+// D = 128, 75 MB: 11.5 at the copy rate; 33.0 us in fp32, 134 MB: 20.4).  K words are 8
+// channels of a token, one 16-byte store (bf16) each; a V thread turns 8 channels x 8 tokens
+// in registers.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) unpack_kernel(const uint8_t *hist, long long cap, int first_chunk,
                                                           int n_chunks, T *k, T *v, long long head_stride) {
@@ -546,8 +548,8 @@ __global__ void __launch_bounds__(kThreads) unpack_kernel(const uint8_t *hist, l
         uint32_t s[4], z[4], r[4];
         load4(rec + P::kGridOff + 16 * o, s);
         load4(rec + P::kGridOff + P::kGridHalf + 16 * o, z);
-        // a load may not pass a store: four words at once (all eight or sixteen: 35.5 us for
-        // 1,792 fp32 chunks against 33.4)
+        // a load may not pass a store: four words at once (all eight of D = 128: 35.5 us for
+        // 1,792 fp32 chunks against 33.0)
         constexpr int STEP = kThreads / 2 / OPR, AT_ONCE = 4;
 #pragma unroll
         for (int row = 0; row < kChunk; row += AT_ONCE * STEP) {

@@ -581,7 +581,8 @@ hga_status_t hga_rope_table(double theta, int rotary_dim, long long n_pos, float
  *   n = x * w / sqrt(mean(x^2) + eps)
  *   y_i = n_i c_i - n_{i+R/2} s_i,  y_{i+R/2} = n_{i+R/2} c_i + n_i s_i   (i < R/2)
  * with c_i, s_i from row pos of table; dims >= R are n; v is copied.  fp32
- * arithmetic, one rounding to dtype.
+ * arithmetic, one rounding to dtype (a row whose squares pass the range of fp32,
+ * |x| above 1e19, has n = 0).
  *   q, k, v: device, token rows as in hga_proj_t.  q_weight, k_weight: device [D]
  *     dtype.  table: device fp32 [n_pos][R] (hga_rope_table; may be null for R = 0).
  *   positions: device int32 [B][S], or null for first_pos + i (then first_pos >= 0
@@ -602,7 +603,8 @@ hga_status_t hga_qk_norm_rope(const hga_proj_t *p, const void *q, const void *k,
 /* Backward of hga_qk_norm_rope.  dq [B][Hq][S][D], dk and dv [B][Hkv][S][D]: device
  * fp32, as hga_attn_bwd writes them.  With dn the transposed rotation of the
  * incoming row, r = 1 / sqrt(mean(x^2) + eps), xh = x r and g = dn w:
- *   dx = r (g - xh mean(g xh)),   dw = sum over every head row of dn xh.
+ *   dx = r (g - xh mean(g xh)),   dw = sum over every head row of dn xh
+ * (in fp32 over the rows of a thread block, in 64 bits over the blocks).
  *   dq_in, dk_in, dv_in: device dtype, rows and strides of q, k, v (the operands of
  *     the projections' products, so they are rounded to dtype); padding rows get
  *     zeros.  dq_weight, dk_weight: device fp32 [D], overwritten.
@@ -627,7 +629,8 @@ hga_status_t hga_qk_norm_rope_bwd(const hga_proj_t *p, const void *q, const void
  *   V codes  uint32 [D channels][8]: word w of a channel holds tokens 8w .. 8w + 7
  *   V grid   bf16 s[D/64][64], z[D/64][64]: a pair per 64 channels and token
  * Nibble j < 4 of a word is its element 2j, nibble 4 + j its element 2j + 1.  Code c
- * stands for bf16(s (16 + c) + z), rounded once.  For a group (one pair's elements)
+ * stands for bf16(s (16 + c) + z), rounded once (to an infinity beyond the range
+ * of bf16).  For a group (one pair's elements)
  * with extremes mn, mx:
  *   s = bf16(fl32(fl32(mx - mn) fl32(1/15))), 0 if below 2^-100;  z = bf16(fl32(mn - 16 s));
  *   c = the code nearest to the element, (x - z) / s - 16 rounded to even in 0 .. 15.
@@ -636,7 +639,7 @@ hga_status_t hga_qk_norm_rope_bwd(const hga_proj_t *p, const void *q, const void
  * with an element that is not finite (or whose s or z overflows) reads back as NaN.
  *   hist: device, 16-byte aligned, [B][Hkv][hist_cap_chunks] records.
  * The attention calls below attend exactly the values that hga_unpack_history
- * returns; a backward pass (or any other call of this header) over packed history
+ * returns, with P rounded to bf16 for the P.V product as in hga_attn_fwd; a backward pass (or any other call of this header) over packed history
  * unpacks the chunks it needs first. */
 size_t hga_packed_chunk_bytes(int head_dim);
 
