@@ -213,9 +213,10 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
-def _check(rc: int, what: str):
+def _check(rc: int, what: str, reason: bool = False):
+    """Raises for a status; ``reason``: the call leaves the text of its own refusals, or none."""
     if rc != 0:
-        detail = lib().hga_last_error().decode() if rc == -3 else ""
+        detail = lib().hga_last_error().decode() if rc == -3 or reason else ""
         raise HGAError(rc, what, detail)
 
 
@@ -646,7 +647,7 @@ def hga_attn_fwd_packed(p: Params, q, hist, hist_cap_chunks: int, k_seg, v_seg, 
     _attn_types("hga_attn_fwd_packed", p, q, k_seg, v_seg, idx, out, lse)
     _check(lib().hga_attn_fwd_packed(p.ref(), _ptr(q), _ptr(hist), hist_cap_chunks, _ptr(k_seg),
                                      _ptr(v_seg), _ptr(idx), _ptr(out), _ptr(lse), _stream(stream)),
-           "hga_attn_fwd_packed")
+           "hga_attn_fwd_packed", reason=True)
 
 
 def hga_attn_decode_packed(p: Params, q, hist, hist_cap_chunks: int, k_local, v_local, n_local: int, idx, out, lse,
@@ -655,7 +656,7 @@ def hga_attn_decode_packed(p: Params, q, hist, hist_cap_chunks: int, k_local, v_
     _attn_types("hga_attn_decode_packed", p, q, k_local, v_local, idx, out, lse)
     _check(lib().hga_attn_decode_packed(p.ref(), _ptr(q), _ptr(hist), hist_cap_chunks, _ptr(k_local),
                                         _ptr(v_local), n_local, _ptr(idx), _ptr(out), _ptr(lse), _stream(stream)),
-           "hga_attn_decode_packed")
+           "hga_attn_decode_packed", reason=True)
 
 
 def hga_get_device_status(stream=None) -> int:

@@ -877,6 +877,7 @@ hga_status_t hga_attn_fwd_packed(const hga_params_t *p, const void *q, const voi
                                  const void *k_seg, const void *v_seg, const int32_t *idx, void *out, float *lse,
                                  cudaStream_t stream) {
     CallRange range("hga_attn_fwd_packed");
+    hga::record_error("");  // a refusal's text is this call's
     hga_status_t st = check_params(p);
     if (st != HGA_OK) return st;
     if (p->q_block != 64) return HGA_ERR_UNSUPPORTED;  // one-token segments go through hga_attn_decode_packed
@@ -904,6 +905,7 @@ hga_status_t hga_attn_decode_packed(const hga_params_t *p, const void *q, const 
                                     const void *k_local, const void *v_local, int n_local, const int32_t *idx,
                                     void *out, float *lse, cudaStream_t stream) {
     CallRange range("hga_attn_decode_packed");
+    hga::record_error("");
     hga_status_t st = check_params(p);
     if (st != HGA_OK) return st;
     if (p->seg_len != 1 || p->q_block != 1) return HGA_ERR_UNSUPPORTED;

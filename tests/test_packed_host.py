@@ -367,3 +367,24 @@ def test_params_struct_of_any_number():
     for name in names:
         setattr(swapped, name, fields[name])
     assert struct(swapped).topk == 64 and struct(swapped).seg_len == 4
+
+
+def test_refusals_of_packed_attention_say_why():
+    """The library's reason reaches the Python error, and only that call's."""
+    import torch
+    hist, idx = torch.zeros(72 * 64, dtype=torch.uint8), torch.zeros(1, 1, 1, 1, dtype=torch.int32)
+
+    def call(n, heads, dtype, topk=1):
+        p = hga.Params(1, heads, 1, 64, topk, n, 1, q_block=n, dtype=hga.HGA_FP32 if dtype == torch.float32 else hga.HGA_BF16)
+        q, kv, lse = torch.zeros(1, heads, n, 64, dtype=dtype), torch.zeros(1, 1, n, 64, dtype=dtype), torch.zeros(1, heads, n)
+        with pytest.raises(hga.HGAError) as e:
+            if n == 1:
+                hga.hga_attn_decode_packed(p, q, hist, 1, kv, kv.clone(), 1, idx, q.clone(), lse, stream=0)
+            else:
+                hga.hga_attn_fwd_packed(p, q, hist, 1, kv, kv.clone(), idx, q.clone(), lse, stream=0)
+        return str(e.value)
+
+    assert "8 query heads" in call(1, 9, torch.bfloat16)
+    assert "8 query heads" not in call(1, 1, torch.bfloat16, topk=0)  # another refusal
+    assert "bf16 only" in call(64, 1, torch.float32)
+    assert "bf16 only" not in call(64, 1, torch.bfloat16, topk=0)
