@@ -5,7 +5,7 @@
 // exact chunks next to a local window), with the history's values as packed.cuh defines
 // them: z_t = q . k_t / sqrt(D), out = sum_t softmax(z)_t v_t.
 //
-// Bound by HBM, and at small batches by latency: a routed chunk is 72 D bytes (0.28 of
+// The floor is HBM, and at small batches latency: a routed chunk is 72 D bytes (0.28 of
 // bf16), read once for the G <= 8 query heads of its KV head.  A warp takes a whole chunk.
 // Its record comes as one bulk copy into the warp's own two-stage ring in shared memory, so
 // the next record is on its way while this one is multiplied, and no register holds data in
